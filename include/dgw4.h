@@ -410,6 +410,115 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
                                  void *stream);
 
 /*
+ * dgw4_moe_few — the routed-expert layer of dgw4_moe_forward for few tokens,
+ * in two launches: at most 512 assignments (T * topk; 64 tokens at top-8).
+ * Each launch splits the chosen experts' weights over the whole chip, where
+ * dgw4_moe_forward gives half an expert to one workgroup: the form for one
+ * token to a few dozen. The formula, the packed weights in either layout and
+ * the treatment of ids (outside [0, E): no contribution; equal ids: each
+ * counts) are dgw4_moe_forward's. Sums are fp32, each group's scale applied
+ * to an fp32 partial sum of exact integers times x; the gated intermediate is
+ * rounded to fp16 once, the expert outputs stay in fp32 until they are
+ * weighted and added in ascending k, and out is rounded to fp16 once. The
+ * results agree with dgw4_moe_forward's up to rounding and repeated calls
+ * give identical bits. A row of x that no live id names is not read into any
+ * other row's result; a token without live ids gets zeros.
+ *   T >= 0, 1 <= topk <= E, 1 <= E <= 1024, d % gu_g == 0, m % dn_g == 0;
+ *   gu_g, dn_g: 64 or 128, each or-ed with DGW4_WEIGHTS_TILED where that
+ *   stack is tiled; the DGW4_ROWS_* bits are refused (INVALID_ARG).
+ *   T * topk > 512, or x, the intermediate or one expert's weights from
+ *   2 GiB: DGW4_ERR_UNSUPPORTED.
+ * Pointers, alignment (x, the six pack arrays 16 bytes, out 8, workspace
+ * 256) and the workspace query (workspace == NULL writes *ws_bytes) as for
+ * dgw4_moe_forward; the workspace is this call's own (calls that may overlap
+ * need one each) and its size differs from dgw4_moe_forward's.
+ */
+DGW4_API int dgw4_moe_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int T,
+                          int topk, int E, int d, int m, const uint8_t *gu_q, const uint16_t *gu_s,
+                          const uint16_t *gu_z, int gu_g, const uint8_t *dn_q,
+                          const uint16_t *dn_s, const uint16_t *dn_z, int dn_g, void *workspace,
+                          size_t *ws_bytes, uint16_t *out, void *stream);
+
+/*
+ * dgw4_moe_few_routed — dgw4_moe_few from router logits (device fp32 [T, E],
+ * finite, 4-byte aligned; topk <= 64): the same ids and weights as
+ * dgw4_router's, then the layer. The same workspace size and the same bits as
+ * dgw4_router followed by dgw4_moe_few.
+ */
+DGW4_API int dgw4_moe_few_routed(const uint16_t *x, const float *router_logits, int T, int topk,
+                                 int E, int d, int m, const uint8_t *gu_q, const uint16_t *gu_s,
+                                 const uint16_t *gu_z, int gu_g, const uint8_t *dn_q,
+                                 const uint16_t *dn_s, const uint16_t *dn_z, int dn_g,
+                                 void *workspace, size_t *ws_bytes, uint16_t *out, void *stream);
+
+/* Element types of the 8-bit entry points' activations and outputs. */
+#define DGW4_F32 0
+#define DGW4_F16 1
+#define DGW4_BF16 2
+
+/*
+ * dgw4_quantize_rows_i8 — symmetric 8-bit quantisation of rows, one fp32
+ * scale each: a token's activations, or an output channel's weights. Per row,
+ * in fp32 with IEEE round-to-nearest-even:
+ *   s = max|x| / 127; s = 1 if that is zero
+ *   q = clamp(rint(x / s), -127, 127)
+ * A row that holds a NaN or an infinity gets s = NaN and q = 0, so that every
+ * product with it is NaN. Exact and deterministic.
+ *   x       device, x_type (DGW4_F32, DGW4_F16, DGW4_BF16) [rows, K], rows
+ *           ldx elements apart (ldx >= K), aligned to its element
+ *   rows >= 0, K >= 1
+ *   q       device int8 [rows, Kp] (output), Kp = K rounded up to 16, rows
+ *           ldq bytes apart (ldq >= Kp, ldq % 16 == 0), 16-byte aligned; columns
+ *           K .. Kp - 1 are set to 0, later ones left as they are
+ *   s       device fp32 [rows] (output)
+ * x and q must not overlap. rows == 0 is a no-op. Enqueued on `stream`.
+ */
+DGW4_API int dgw4_quantize_rows_i8(const void *x, int x_type, int rows, int K, long long ldx,
+                                   int8_t *q, long long ldq, float *s, void *stream);
+
+/*
+ * dgw4_w8a8_linear — the dense layer on 8-bit rows:
+ *   y[t, n] = (sum_k xq[t, k] * wq[n, k]) * xs[t] * ws[n]
+ * with one scale per token and one per output channel. The sum is an exact
+ * 32-bit integer; it is rounded to fp32, multiplied by xs[t], then by ws[n]
+ * (each product rounded to fp32), and rounded to y's type once: the result
+ * does not depend on the order of the sum, and repeated calls give identical
+ * bits.
+ *   xq  device int8 [T, K], rows ldx bytes apart; xs device fp32 [T]
+ *   wq  device int8 [N, K], rows ldw bytes apart; ws device fp32 [N]
+ *       (any int8 values; xq, wq 16-byte aligned; ldx, ldw >= K and % 16 == 0)
+ *   y   device y_type [T, N] (output), rows ldy elements apart (ldy >= N),
+ *       aligned to its element; elements between the rows are left as they are
+ *   T >= 0, N >= 1 of any value; K >= 16, K % 16 == 0 (rows of
+ *   dgw4_quantize_rows_i8 are zero-padded to that), K <= 131056 (the sum fits
+ *   32 bits for all codes); ldx, ldw <= 2^22. DGW4_ERR_UNSUPPORTED where K or a
+ *   row distance is out of these ranges, DGW4_ERR_INVALID_ARG for the rest.
+ * T == 0 is a no-op. Enqueued on `stream`.
+ */
+DGW4_API int dgw4_w8a8_linear(const int8_t *xq, const float *xs, int T, int K, long long ldx,
+                              const int8_t *wq, const float *ws, int N, long long ldw, void *y,
+                              int y_type, long long ldy, void *stream);
+
+/*
+ * dgw4_w8a8_linear_tokens — dgw4_w8a8_linear from activations: each row of x
+ * is quantised as dgw4_quantize_rows_i8 does, then multiplied; the same bits
+ * as the two calls. A few tokens are quantised inside the product's own
+ * launch, more in a launch before it.
+ *   x   device, x_type [T, K], rows ldx elements apart (ldx >= K), aligned to
+ *       its element; K >= 1
+ *   wq  device int8 [N, Kp], Kp = K rounded up to 16, as above (the values of
+ *       its columns K .. Kp - 1 do not matter)
+ *   workspace  device scratch of *ws_bytes bytes, 256-byte aligned, this call's
+ *       own; workspace == NULL writes the required size to *ws_bytes and
+ *       launches nothing
+ * The rest as for dgw4_w8a8_linear; x and y must not overlap.
+ */
+DGW4_API int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, long long ldx,
+                                     const int8_t *wq, const float *ws, int N, long long ldw,
+                                     void *y, int y_type, long long ldy, void *workspace,
+                                     size_t *ws_bytes, void *stream);
+
+/*
  * dgw4_hbm_read_probe — a measurement aid, not a step of the layer: reads
  * `bytes` bytes of device memory at `buf` once, with the whole chip
  * (16-byte non-temporal loads, several in flight per lane), so that the elapsed time on

@@ -1,0 +1,234 @@
+"""GPU: 8-bit row quantisation and the 8-bit products against their
+definitions, bit for bit (the sums are exact integers and every rounding is
+stated, so there is one right answer; tests/few_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import w4a16_grouped_moe_amd as dg
+from tests import few_ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm device")
+    dg.lib()
+
+
+def _acts(rng, rows, K, dtype):
+    x = torch.from_numpy(rng.standard_normal((rows, K), dtype=np.float32))
+    x *= torch.from_numpy(np.exp(rng.standard_normal(K)).astype(np.float32))
+    return x.to(dtype)
+
+
+def _codes(rng, rows, K, low=-127):
+    q = rng.integers(low, 128, (rows, K), dtype=np.int8)
+    s = np.exp(rng.standard_normal(rows) - 5).astype(np.float32)
+    return q, s
+
+
+def _dev(*a):
+    return [torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in a]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 16), (3, 17), (5, 2816), (300, 100), (2, 16384),
+                                    (7, 4097), (2, 70001), (1000, 33)])
+def test_quantize_rows(rows, K, dtype):
+    rng = np.random.default_rng([rows, K])
+    x = _acts(rng, rows, K, dtype)
+    q, s = dg.quantize_rows_i8(x.cuda())
+    rq, rs = few_ref.quantize_rows(x)
+    assert q.shape == rq.shape
+    assert np.array_equal(q.cpu().numpy(), rq)
+    assert np.array_equal(s.cpu().numpy().view(np.int32), rs.view(np.int32))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_quantize_edges(dtype):
+    # zeros, one sign, ties of the rounding, the type's extremes and subnormals,
+    # NaN and infinities: each row on its own
+    K = 300
+    fi = torch.finfo(dtype)
+    x = torch.zeros((12, K), dtype=dtype)
+    x[1, 7] = -3
+    x[2] = torch.arange(K).to(dtype) - 100
+    x[3, :4] = torch.tensor([127.0, 0.5, 1.5, -2.5]).to(dtype)
+    x[3, 4:130] = (torch.arange(126) + 0.5).to(dtype)
+    x[4, 3] = fi.max
+    x[4, 4] = -fi.max
+    x[5, 3] = fi.tiny
+    x[6, 250] = fi.smallest_normal * fi.eps          # the smallest subnormal
+    x[6, 251] = -3 * fi.smallest_normal * fi.eps
+    x[7, 299] = float("nan")
+    x[8, 0] = float("inf")
+    x[9, 1] = float("-inf")
+    x[10, 2], x[10, 3] = float("nan"), float("inf")
+    x[11] = -0.0
+    x[7:11, 9] = 2
+    q, s = dg.quantize_rows_i8(x.cuda())
+    rq, rs = few_ref.quantize_rows(x)
+    assert np.array_equal(q.cpu().numpy(), rq)
+    assert few_ref.same_bits(s, torch.from_numpy(rs))
+    assert torch.isnan(s[7:11]).all() and (s[[0, 11]] == 1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("skip", [1, 3, 8, 13])
+def test_quantize_strided(dtype, skip):
+    # rows apart, from an odd element on; outputs into slices, the rest untouched
+    rng = np.random.default_rng(skip)
+    wide = _acts(rng, 21, 150 + skip, dtype).cuda()
+    x = wide[:, skip:]
+    q = torch.full((23, 192), 55, dtype=torch.int8, device="cuda")
+    s = torch.full((23,), 9.0, device="cuda")
+    dg.quantize_rows_i8(x, out=(q[:21, 16:176], s[:21]))
+    rq, rs = few_ref.quantize_rows(x.cpu())
+    assert np.array_equal(q[:21, 16:176].cpu().numpy(), rq)
+    assert np.array_equal(s[:21].cpu().numpy(), rs)
+    assert (q[21:] == 55).all() and (q[:, :16] == 55).all() and (q[:, 176:] == 55).all()
+    assert (s[21:] == 9).all()
+
+
+PRODUCTS = [(1, 16, 1), (1, 2816, 300), (2, 64, 17), (3, 4096, 64), (5, 48, 1000), (8, 704, 129),
+            (16, 1024, 255), (17, 2816, 77), (31, 80, 33), (33, 16384, 40), (64, 256, 256),
+            (65, 272, 515), (100, 1008, 90), (128, 704, 513), (200, 128, 1030), (257, 320, 257),
+            (300, 2816, 700), (513, 144, 260), (1030, 64, 31), (1, 131056, 5), (40, 131056, 18)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,K,N", PRODUCTS)
+def test_product(T, K, N, dtype):
+    rng = np.random.default_rng([T, K, N])
+    (xq, xs), (wq, ws) = _codes(rng, T, K), _codes(rng, N, K)
+    xd, sd, wd, vd = _dev(xq, xs, wq, ws)
+    y = dg.w8a8_linear(xd, sd, (wd, vd), dtype=dtype)
+    assert few_ref.same_bits(y, few_ref.product(xq, xs, wq, ws, dtype))
+
+
+@pytest.mark.parametrize("T", [1, 9, 70, 300])
+def test_product_extremes(T):
+    # the largest sums (all codes -128 at the longest K), zeros, and scales
+    # whose products overflow, vanish or are NaN
+    K, N = 131056, 34
+    xq = np.full((T, K), -128, dtype=np.int8)
+    wq = np.full((N, K), -128, dtype=np.int8)
+    wq[1] = 127
+    wq[2] = 0
+    xs = np.geomspace(1e-30, 1e30, T).astype(np.float32)
+    xs[0] = np.nan
+    ws = np.geomspace(1e-10, 1e10, N).astype(np.float32)
+    xd, sd, wd, vd = _dev(xq, xs, wq, ws)
+    for dtype in TYPES:
+        y = dg.w8a8_linear(xd, sd, (wd, vd), dtype=dtype)
+        assert few_ref.same_bits(y, few_ref.product(xq, xs, wq, ws, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,K,N,pad", [(3, 64, 50, 5), (40, 96, 130, 3), (150, 192, 300, 1),
+                                       (260, 128, 256, 8)])
+def test_product_strided(T, K, N, pad, dtype):
+    # operands and output inside wider tensors; what lies between stays
+    rng = np.random.default_rng([T, N])
+    xq, xs = _codes(rng, T, K + 48)
+    wq, ws = _codes(rng, N, K + 32)
+    xd, sd, wd, vd = _dev(xq, xs, wq, ws)
+    big = torch.full((T + 2, N + 2 * pad), 3.0, dtype=dtype, device="cuda")
+    y = big[1:T + 1, pad:pad + N]
+    dg.w8a8_linear(xd[:, 32:32 + K], sd, (wd[:, 16:16 + K], vd), out=y)
+    assert few_ref.same_bits(y, few_ref.product(xq[:, 32:32 + K], xs, wq[:, 16:16 + K], ws, dtype))
+    assert (big[0] == 3).all() and (big[-1] == 3).all()
+    assert (big[:, :pad] == 3).all() and (big[:, pad + N:] == 3).all()
+
+
+@pytest.mark.parametrize("xtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,K,N", [(1, 1, 1), (1, 2816, 512), (1, 16384, 100), (2, 100, 65), (4, 2816, 1000),
+                                   (8, 17, 300), (13, 2000, 48), (16, 333, 257), (17, 500, 70),
+                                   (130, 2816, 300), (3, 70001, 20)])
+def test_product_from_activations(T, K, N, xtype):
+    rng = np.random.default_rng([T, K, N, 1])
+    x = _acts(rng, T, K, xtype)
+    Kp = (K + 15) // 16 * 16
+    wq, ws = _codes(rng, N, Kp)                   # the columns past K hold anything
+    wd, vd = _dev(wq, ws)
+    rq, rs = few_ref.quantize_rows(x)
+    n = dg.w8a8_workspace_bytes(T, K)
+    ws_buf = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    for dtype in TYPES:
+        y = dg.w8a8_linear_tokens(x.cuda(), (wd, vd), dtype=dtype, workspace=ws_buf)
+        assert few_ref.same_bits(y, few_ref.product(rq, rs, wq, ws, dtype)), dtype
+        q, s = dg.quantize_rows_i8(x.cuda())
+        assert few_ref.same_bits(y, dg.w8a8_linear(q, s, (wd, vd), dtype=dtype))
+
+
+@pytest.mark.parametrize("T", [2, 9, 40])
+def test_activations_strided_and_nonfinite(T):
+    rng = np.random.default_rng(T)
+    wide = _acts(rng, T, 403, torch.bfloat16)
+    wide[T // 2, 200] = float("nan")
+    wide[0, 300] = float("inf")
+    x = wide[:, 3:]
+    wq, ws = _codes(rng, 70, 400)
+    wd, vd = _dev(wq, ws)
+    big = torch.full((T + 1, 75), 3.0, device="cuda")
+    y = dg.w8a8_linear_tokens(wide.cuda()[:, 3:], (wd, vd), out=big[:T, 2:72])
+    rq, rs = few_ref.quantize_rows(x)
+    assert few_ref.same_bits(y, few_ref.product(rq, rs, wq, ws, torch.float32))
+    assert torch.isnan(y[0]).all() and torch.isnan(y[T // 2]).all()
+    assert (big[T] == 3).all() and (big[:, :2] == 3).all() and (big[:, 72:] == 3).all()
+
+
+def test_empty_batch():
+    w = (torch.zeros((8, 32), dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))
+    assert dg.w8a8_linear(w[0][:0], w[1][:0], w).shape == (0, 8)
+    assert dg.w8a8_linear_tokens(torch.empty((0, 32), device="cuda"), w).shape == (0, 8)
+    q, s = dg.quantize_rows_i8(torch.empty((0, 20), device="cuda"))
+    assert q.shape == (0, 32) and s.shape == (0,)
+
+
+def test_offsets_past_32_bits():
+    # outputs, weights and activations whose byte offsets pass 2^32: the last
+    # rows and columns of each
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60 << 30:
+        pytest.skip("needs 60 GiB")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    # weights of 4.3 GB
+    N, K = 33000, 131056
+    wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    ws = torch.rand(N, device="cuda", generator=g)
+    for T in (2, 40):
+        xq = torch.randint(-127, 128, (T, K), dtype=torch.int8, device="cuda", generator=g)
+        xs = torch.rand(T, device="cuda", generator=g)
+        y = dg.w8a8_linear(xq, xs, (wq, ws), dtype=torch.float32)
+        for n0 in (0, N - 40):
+            ref = few_ref.product(xq.cpu().numpy(), xs.cpu().numpy(), wq[n0:n0 + 40].cpu().numpy(),
+                                  ws[n0:n0 + 40].cpu().numpy(), torch.float32)
+            assert few_ref.same_bits(y[:, n0:n0 + 40], ref), (T, n0)
+    # activations of 4.3 GB, quantised and multiplied as they are
+    wq2, ws2 = wq[:20].contiguous(), ws[:20].contiguous()
+    xs = torch.rand(N, device="cuda", generator=g)
+    y = dg.w8a8_linear(wq, xs, (wq2, ws2), dtype=torch.float32)
+    ref = few_ref.product(wq[-50:].cpu().numpy(), xs[-50:].cpu().numpy(), wq2.cpu().numpy(),
+                          ws2.cpu().numpy(), torch.float32)
+    assert few_ref.same_bits(y[-50:], ref)
+    del wq, y
+    # an output of 4.4 GB
+    T, N, K = 4200, 262144, 16
+    xq = torch.randint(-127, 128, (T, K), dtype=torch.int8, device="cuda", generator=g)
+    wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    xs, ws = torch.rand(T, device="cuda", generator=g), torch.rand(N, device="cuda", generator=g)
+    y = dg.w8a8_linear(xq, xs, (wq, ws), dtype=torch.float32)
+    ref = few_ref.product(xq[-60:].cpu().numpy(), xs[-60:].cpu().numpy(), wq[-300:].cpu().numpy(),
+                          ws[-300:].cpu().numpy(), torch.float32)
+    assert few_ref.same_bits(y[-60:, -300:], ref)
+    # rows of activations past 2^32 bytes
+    x = torch.randn((70000, 16384), dtype=torch.float32, device="cuda", generator=g)
+    q, s = dg.quantize_rows_i8(x)
+    rq, rs = few_ref.quantize_rows(x[-3:].cpu())
+    assert np.array_equal(q[-3:].cpu().numpy(), rq) and np.array_equal(s[-3:].cpu().numpy(), rs)

@@ -8,6 +8,7 @@ an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -83,6 +84,18 @@ def lib():
         L.dgw4_sample_noalloc.argtypes = [P, I, I, ctypes.c_uint64, P, P, P, P]
         L.dgw4_pack_tiled.restype = I
         L.dgw4_pack_tiled.argtypes = [P, I, I, I, I, P, P]
+        LL = ctypes.c_longlong
+        L.dgw4_moe_few.restype = I
+        L.dgw4_moe_few.argtypes = L.dgw4_moe_forward.argtypes
+        L.dgw4_moe_few_routed.restype = I
+        L.dgw4_moe_few_routed.argtypes = L.dgw4_moe_forward_routed.argtypes
+        L.dgw4_quantize_rows_i8.restype = I
+        L.dgw4_quantize_rows_i8.argtypes = [P, I, I, I, LL, P, LL, P, P]
+        L.dgw4_w8a8_linear.restype = I
+        L.dgw4_w8a8_linear.argtypes = [P, P, I, I, LL, P, P, I, LL, P, I, LL, P]
+        L.dgw4_w8a8_linear_tokens.restype = I
+        L.dgw4_w8a8_linear_tokens.argtypes = [P, I, I, I, LL, P, P, I, LL, P, I, LL, P,
+                                              ctypes.POINTER(S), P]
         L.dgw4_hbm_read_probe.restype = I
         L.dgw4_hbm_read_probe.argtypes = [P, S, P, P]
         L.dgw4_mfma_probe.restype = I
@@ -492,3 +505,212 @@ def moe_forward_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, 
         ptrs[7], dg, pws, ctypes.byref(n), pout, _stream(x)))
     return out
 
+
+
+def moe_few_workspace_bytes(T: int, topk: int, E: int, d: int, m: int, gu_g: int = 128,
+                            dn_g: int = 64) -> int:
+    """Device workspace moe_few and moe_few_routed need (host-only query)."""
+    n = ctypes.c_size_t(0)
+    _check("dgw4_moe_few(query)", lib().dgw4_moe_few(
+        None, None, None, T, topk, E, d, m, None, None, None, gu_g, None, None, None, dn_g,
+        None, ctypes.byref(n), None, None))
+    return int(n.value)
+
+
+def _same_device(t: torch.Tensor, **others) -> None:
+    for name, o in others.items():
+        if o.device != t.device:
+            raise ValueError(f"{name} is on {o.device}, not {t.device}")
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device as the current one while a call is enqueued."""
+    if torch.cuda.current_device() == t.device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, out) -> torch.Tensor:
+    """The arguments that moe_few and moe_few_routed share; route = their
+    routing tensors (checked by the caller)."""
+    gq, gs, gz, gg = gu
+    dq, ds, dz, dg = dn
+    if x.dim() != 2 or gq.dim() != 3 or dq.dim() != 3:
+        raise ValueError("x must be [T, d], the packed stacks [E, N, K/2]")
+    T, d = x.shape
+    E = gq.shape[0]
+    m = dq.shape[2] * 2
+    if gq.shape != (E, 2 * m, d // 2) or dq.shape != (E, d, m // 2):
+        raise ValueError(f"packed shapes {tuple(gq.shape)} / {tuple(dq.shape)} do not match "
+                         f"x {tuple(x.shape)}")
+    if _group(gg) < 1 or _group(dg) < 1:
+        raise ValueError("group sizes must be positive")
+    if gs.shape != (E, 2 * m, d // _group(gg)) or gz.shape != gs.shape:
+        raise ValueError("gate_up scale/zero shape mismatch")
+    if ds.shape != (E, d, m // _group(dg)) or dz.shape != ds.shape:
+        raise ValueError("down scale/zero shape mismatch")
+    ptrs = [_dev(x, "x", _F16), *(_dev(t, n, ty) for t, n, ty in route),
+            _dev(gq, "gu_q", (torch.uint8,)), _dev(gs, "gu_s", _F16), _dev(gz, "gu_z", _F16),
+            _dev(dq, "dn_q", (torch.uint8,)), _dev(ds, "dn_s", _F16), _dev(dz, "dn_z", _F16)]
+    if workspace is None:
+        need = moe_few_workspace_bytes(T, topk, E, d, m, gg, dg)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    pws = _dev(workspace, "workspace", (torch.uint8,))
+    if out is None:
+        out = torch.empty((T, d), dtype=torch.float16, device=x.device)
+    if out.shape != (T, d):
+        raise ValueError("out must be [T, d]")
+    pout = _dev(out, "out", _F16)
+    _same_device(x, gu_q=gq, gu_s=gs, gu_z=gz, dn_q=dq, dn_s=ds, dn_z=dz, workspace=workspace,
+                 out=out, **{n: t for t, n, _ in route})
+    n = ctypes.c_size_t(workspace.numel())
+    i = 1 + len(route)
+    with _on(x):
+        _check(fn, getattr(lib(), fn)(
+            *ptrs[:i], T, topk, E, d, m, ptrs[i], ptrs[i + 1], ptrs[i + 2], gg, ptrs[i + 3],
+            ptrs[i + 4], ptrs[i + 5], dg, pws, ctypes.byref(n), pout, _stream(x)))
+    return out
+
+
+def moe_few(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, gu: tuple, dn: tuple,
+            workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The routed-expert layer for few tokens (T * topk <= 512), in two
+    launches that split the chosen experts' weights over the whole chip.
+
+    Arguments as for moe_forward (see dgw4_moe_few in include/dgw4.h);
+    ``workspace``: uint8 of at least moe_few_workspace_bytes(...), allocated
+    here when not given. Returns out fp16 [T, d]."""
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != x.shape[0] or topk_w.shape != topk_ids.shape:
+        raise ValueError("topk_ids / topk_weights must be [T, topk]")
+    return _few("dgw4_moe_few", x, ((topk_ids, "topk_ids", (torch.int32,)),
+                                    (topk_w, "topk_w", (torch.float32,))),
+                topk_ids.shape[1], gu, dn, workspace, out)
+
+
+def moe_few_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, gu: tuple, dn: tuple,
+                   workspace: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_few from router logits fp32 [T, E]: the same bits as router()
+    followed by moe_few()."""
+    if router_logits.shape != (x.shape[0], gu[0].shape[0]):
+        raise ValueError("router_logits must be [T, E]")
+    return _few("dgw4_moe_few_routed", x, ((router_logits, "router_logits", (torch.float32,)),),
+                int(topk), gu, dn, workspace, out)
+
+
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _rows(t: torch.Tensor, name: str, dtypes) -> tuple[int, int]:
+    """Pointer and row distance of a 2-d device tensor whose rows are
+    contiguous but may lie apart (a slice of a wider tensor)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a ROCm device, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name}: the elements of a row must be contiguous, its rows must not overlap")
+    return t.data_ptr(), ld
+
+
+def _up16(k: int) -> int:
+    return (k + 15) // 16 * 16
+
+
+def quantize_rows_i8(x: torch.Tensor, out: tuple | None = None):
+    """Symmetric 8-bit quantisation of each row of x (fp32, fp16 or bf16
+    [rows, K]; rows may lie apart): (q int8 [rows, K rounded up to 16], the
+    added columns zero, s fp32 [rows]). ``out`` = (q, s) to write into."""
+    px, ldx = _rows(x, "x", _TYPES)
+    rows, K = x.shape
+    if out is None:
+        out = (torch.empty((rows, _up16(K)), dtype=torch.int8, device=x.device),
+               torch.empty(rows, dtype=torch.float32, device=x.device))
+    q, s = out
+    pq, ldq = _rows(q, "q", (torch.int8,))
+    ps = _dev(s, "s", (torch.float32,))
+    if q.shape != (rows, _up16(K)) or s.shape != (rows,):
+        raise ValueError("out must be (q [rows, K rounded up to 16], s [rows])")
+    _same_device(x, q=q, s=s)
+    with _on(x):
+        _check("dgw4_quantize_rows_i8", lib().dgw4_quantize_rows_i8(
+            px, _TYPES[x.dtype], rows, K, ldx, pq, ldq, ps, _stream(x)))
+    return q, s
+
+
+def _w8a8_out(x, N: int, dtype, out):
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype {dtype} not in {tuple(_TYPES)}")
+        out = torch.empty((x.shape[0], N), dtype=dtype, device=x.device)
+    elif out.shape != (x.shape[0], N):
+        raise ValueError("out must be [T, N]")
+    return out, *_rows(out, "out", _TYPES)
+
+
+def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
+                dtype: torch.dtype = torch.float16) -> torch.Tensor:
+    """y[t, n] = (sum_k xq[t, k] wq[n, k]) * xs[t] * ws[n], exact integer sums.
+
+    xq int8 [T, K] and xs fp32 [T], w = (wq int8 [N, K], ws fp32 [N]), each
+    e.g. of quantize_rows_i8 (K a multiple of 16). Returns y [T, N] of
+    ``dtype`` (fp16, bf16, fp32), or written into ``out``, whose type counts
+    then. See dgw4_w8a8_linear in include/dgw4.h."""
+    wq, ws = w
+    px, ldx = _rows(xq, "xq", (torch.int8,))
+    pw, ldw = _rows(wq, "wq", (torch.int8,))
+    pxs, pws = _dev(xs, "xs", (torch.float32,)), _dev(ws, "ws", (torch.float32,))
+    T, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K or xs.shape != (T,) or ws.shape != (N,):
+        raise ValueError(f"wq {tuple(wq.shape)}, xs {tuple(xs.shape)}, ws {tuple(ws.shape)} do not "
+                         f"match xq {tuple(xq.shape)}")
+    out, py, ldy = _w8a8_out(xq, N, dtype, out)
+    _same_device(xq, xs=xs, wq=wq, ws=ws, out=out)
+    with _on(xq):
+        _check("dgw4_w8a8_linear", lib().dgw4_w8a8_linear(
+            px, pxs, T, K, ldx, pw, pws, N, ldw, py, _TYPES[out.dtype], ldy, _stream(xq)))
+    return out
+
+
+def w8a8_workspace_bytes(T: int, K: int) -> int:
+    """Device workspace w8a8_linear_tokens needs (host-only query)."""
+    n = ctypes.c_size_t(0)
+    _check("dgw4_w8a8_linear_tokens(query)", lib().dgw4_w8a8_linear_tokens(
+        None, 0, T, K, K, None, None, 1, _up16(K), None, 0, 1, None, ctypes.byref(n), None))
+    return int(n.value)
+
+
+def w8a8_linear_tokens(x: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
+                       dtype: torch.dtype = torch.float16,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """w8a8_linear from activations x (fp32, fp16 or bf16 [T, K]; rows may lie
+    apart), each row quantised as quantize_rows_i8 does; the same bits as the
+    two calls. w = (wq int8 [N, K rounded up to 16], ws fp32 [N]).
+    ``workspace``: uint8 of at least w8a8_workspace_bytes(T, K), allocated here
+    when not given."""
+    wq, ws = w
+    px, ldx = _rows(x, "x", _TYPES)
+    pw, ldw = _rows(wq, "wq", (torch.int8,))
+    pws = _dev(ws, "ws", (torch.float32,))
+    T, K = x.shape
+    N = wq.shape[0]
+    if wq.shape[1] != _up16(K) or ws.shape != (N,):
+        raise ValueError(f"wq {tuple(wq.shape)}, ws {tuple(ws.shape)} do not match x {tuple(x.shape)}")
+    out, py, ldy = _w8a8_out(x, N, dtype, out)
+    if workspace is None:
+        workspace = torch.empty(max(w8a8_workspace_bytes(T, K), 1), dtype=torch.uint8, device=x.device)
+    pb = _dev(workspace, "workspace", (torch.uint8,))
+    _same_device(x, wq=wq, ws=ws, out=out, workspace=workspace)
+    n = ctypes.c_size_t(workspace.numel())
+    with _on(x):
+        _check("dgw4_w8a8_linear_tokens", lib().dgw4_w8a8_linear_tokens(
+            px, _TYPES[x.dtype], T, K, ldx, pw, pws, N, ldw, py, _TYPES[out.dtype], ldy, pb,
+            ctypes.byref(n), _stream(x)))
+    return out

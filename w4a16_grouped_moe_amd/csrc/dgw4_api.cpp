@@ -559,6 +559,199 @@ int dgw4_pack_tiled(const uint8_t *q, int E, int N, int K, int g, uint8_t *qt, v
     return from_hip(dgw4::launch_pack_tiled(q, (long long)E * N, K, g, qt, (hipStream_t)stream));
 }
 
+namespace {
+
+// dgw4_moe_few and _routed: checks, workspace (the intermediate, and the
+// router's ids and weights) and launches.
+int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w,
+                 const float *router_logits, bool routed, int T, int topk, int E, int d, int m,
+                 const uint8_t *gu_q, const uint16_t *gu_s, const uint16_t *gu_z, int gu_garg,
+                 const uint8_t *dn_q, const uint16_t *dn_s, const uint16_t *dn_z, int dn_garg,
+                 void *workspace, size_t *ws_bytes, uint16_t *out, void *stream)
+{
+    int gu_g = 0, dn_g = 0, gu_tiled = 0, dn_tiled = 0;
+    if (!split_group(gu_garg, gu_g, gu_tiled) || !split_group(dn_garg, dn_g, dn_tiled))
+        return DGW4_ERR_INVALID_ARG;
+    if (!ws_bytes)
+        return DGW4_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > dgw4::kMaxExperts || topk < 1 || topk > E || d < 1 || m < 1)
+        return DGW4_ERR_INVALID_ARG;
+    if (gu_g < 1 || dn_g < 1 || (routed && topk > 64))
+        return DGW4_ERR_INVALID_ARG;
+    if (!group_supported(gu_g) || !group_supported(dn_g))
+        return DGW4_ERR_UNSUPPORTED;
+    if (d % gu_g != 0 || m % dn_g != 0)
+        return DGW4_ERR_INVALID_ARG;
+    const long long A = (long long)T * topk;
+    // x, the intermediate and one expert's weights are addressed with 32-bit offsets
+    if (A > dgw4::kFewMaxAssign || (long long)T * d * 2 >= (1LL << 31) ||
+        A * m * 2 >= (1LL << 31) || (long long)m * d >= (1LL << 31))
+        return DGW4_ERR_UNSUPPORTED;
+    const size_t h_bytes = round_up(sizeof(uint16_t) * (size_t)A * (size_t)m);
+    const size_t id_bytes = round_up(sizeof(int32_t) * (size_t)A);
+    const size_t need = h_bytes + 2 * id_bytes;
+    if (!workspace) {
+        *ws_bytes = need;
+        return DGW4_OK;
+    }
+    if (!gu_q || !gu_s || !gu_z || !dn_q || !dn_s || !dn_z)
+        return DGW4_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !out || (routed ? !router_logits : !topk_ids || !topk_w)))
+        return DGW4_ERR_INVALID_ARG;
+    if (!aligned(workspace, kAlign) || !aligned(x, 16) || !aligned(gu_q, 16) ||
+        !aligned(dn_q, 16) || !aligned(gu_s, 16) || !aligned(gu_z, 16) || !aligned(dn_s, 16) ||
+        !aligned(dn_z, 16) || !aligned(out, 8) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        !aligned(router_logits, 4))
+        return DGW4_ERR_INVALID_ARG;
+    if (*ws_bytes < need)
+        return DGW4_ERR_WORKSPACE;
+    if (T == 0)
+        return DGW4_OK;
+    char *ws = static_cast<char *>(workspace);
+    dgw4::FewArgs a{};
+    a.x = x;
+    a.ids = topk_ids;
+    a.w = topk_w;
+    a.T = T;
+    a.topk = topk;
+    a.A = (int)A;
+    a.E = E;
+    a.d = d;
+    a.m = m;
+    a.gu_q = gu_q;
+    a.gu_s = gu_s;
+    a.gu_z = gu_z;
+    a.dn_q = dn_q;
+    a.dn_s = dn_s;
+    a.dn_z = dn_z;
+    a.gu_tiled = gu_tiled;
+    a.dn_tiled = dn_tiled;
+    a.h = reinterpret_cast<uint16_t *>(ws);
+    a.out = out;
+    if (routed) {
+        int32_t *rids = reinterpret_cast<int32_t *>(ws + h_bytes);
+        float *rw = reinterpret_cast<float *>(ws + h_bytes + id_bytes);
+        const hipError_t err =
+            dgw4::launch_router(router_logits, T, E, topk, rids, rw, (hipStream_t)stream);
+        if (err != hipSuccess)
+            return from_hip(err);
+        a.ids = rids;
+        a.w = rw;
+    }
+    return from_hip(dgw4::launch_few(a, gu_g, dn_g, (hipStream_t)stream));
+}
+
+// Element size of a DGW4_F32 / F16 / BF16 type; 0 for others.
+size_t type_bytes(int type)
+{
+    return type == DGW4_F32 ? 4 : type == DGW4_F16 || type == DGW4_BF16 ? 2 : 0;
+}
+
+constexpr int kMaxK8 = 131056;              // K * 128 * 128 < 2^31
+constexpr long long kMaxLd8 = 1LL << 22;    // row distances the products address
+
+int up16(int k) { return (k + 15) / 16 * 16; }
+
+// The checks that both forms of the 8-bit product share (Kp: K in whole 16s).
+int w8a8_sizes(int T, int Kp, int N, long long ldw, int y_type, long long ldy)
+{
+    if (T < 0 || Kp < 1 || N < 1 || type_bytes(y_type) == 0 || ldw < Kp || ldw % 16 != 0 || ldy < N)
+        return DGW4_ERR_INVALID_ARG;
+    return Kp > kMaxK8 || ldw > kMaxLd8 ? DGW4_ERR_UNSUPPORTED : DGW4_OK;
+}
+
+}  // namespace
+
+int dgw4_moe_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int T, int topk,
+                 int E, int d, int m, const uint8_t *gu_q, const uint16_t *gu_s,
+                 const uint16_t *gu_z, int gu_g, const uint8_t *dn_q, const uint16_t *dn_s,
+                 const uint16_t *dn_z, int dn_g, void *workspace, size_t *ws_bytes, uint16_t *out,
+                 void *stream)
+{
+    return moe_few_impl(x, topk_ids, topk_w, nullptr, false, T, topk, E, d, m, gu_q, gu_s, gu_z,
+                        gu_g, dn_q, dn_s, dn_z, dn_g, workspace, ws_bytes, out, stream);
+}
+
+int dgw4_moe_few_routed(const uint16_t *x, const float *router_logits, int T, int topk, int E,
+                        int d, int m, const uint8_t *gu_q, const uint16_t *gu_s,
+                        const uint16_t *gu_z, int gu_g, const uint8_t *dn_q, const uint16_t *dn_s,
+                        const uint16_t *dn_z, int dn_g, void *workspace, size_t *ws_bytes,
+                        uint16_t *out, void *stream)
+{
+    return moe_few_impl(x, nullptr, nullptr, router_logits, true, T, topk, E, d, m, gu_q, gu_s,
+                        gu_z, gu_g, dn_q, dn_s, dn_z, dn_g, workspace, ws_bytes, out, stream);
+}
+
+int dgw4_quantize_rows_i8(const void *x, int x_type, int rows, int K, long long ldx, int8_t *q,
+                          long long ldq, float *s, void *stream)
+{
+    const size_t esize = type_bytes(x_type);
+    if (rows < 0 || K < 1 || K > INT_MAX - 16 || esize == 0 || ldx < K || ldq < up16(K) ||
+        ldq % 16 != 0)
+        return DGW4_ERR_INVALID_ARG;
+    if (rows == 0)
+        return DGW4_OK;
+    if (!x || !q || !s || !aligned(x, esize) || !aligned(q, 16) || !aligned(s, 4))
+        return DGW4_ERR_INVALID_ARG;
+    return from_hip(
+        dgw4::launch_quantize_rows(x, x_type, rows, K, ldx, q, ldq, s, (hipStream_t)stream));
+}
+
+int dgw4_w8a8_linear(const int8_t *xq, const float *xs, int T, int K, long long ldx,
+                     const int8_t *wq, const float *ws, int N, long long ldw, void *y, int y_type,
+                     long long ldy, void *stream)
+{
+    if (K < 1 || ldx < K || ldx % 16 != 0)
+        return DGW4_ERR_INVALID_ARG;
+    if (K % 16 != 0 || ldx > kMaxLd8)
+        return DGW4_ERR_UNSUPPORTED;
+    const int st = w8a8_sizes(T, K, N, ldw, y_type, ldy);
+    if (st != DGW4_OK || T == 0)
+        return st;
+    if (!xq || !xs || !wq || !ws || !y || !aligned(xq, 16) || !aligned(wq, 16) ||
+        !aligned(xs, 4) || !aligned(ws, 4) || !aligned(y, type_bytes(y_type)))
+        return DGW4_ERR_INVALID_ARG;
+    const dgw4::I8Args a{xq, xs, wq, ws, T, K, N, ldx, ldw, ldy, y, y_type};
+    return from_hip(dgw4::launch_w8a8_linear(a, (hipStream_t)stream));
+}
+
+int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, long long ldx,
+                            const int8_t *wq, const float *ws, int N, long long ldw, void *y,
+                            int y_type, long long ldy, void *workspace, size_t *ws_bytes,
+                            void *stream)
+{
+    const size_t esize = type_bytes(x_type);
+    if (!ws_bytes || K < 1 || K > INT_MAX - 16 || esize == 0 || ldx < K)
+        return DGW4_ERR_INVALID_ARG;
+    const int Kp = up16(K);
+    const int st = w8a8_sizes(T, Kp, N, ldw, y_type, ldy);
+    if (st != DGW4_OK)
+        return st;
+    const size_t q_bytes = round_up((size_t)T * Kp);
+    const size_t need = q_bytes + round_up((size_t)T * sizeof(float));
+    if (!workspace) {
+        *ws_bytes = need;
+        return DGW4_OK;
+    }
+    if (*ws_bytes < need)
+        return DGW4_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign))
+        return DGW4_ERR_INVALID_ARG;
+    if (T == 0)
+        return DGW4_OK;
+    if (!x || !wq || !ws || !y || !aligned(x, esize) || !aligned(wq, 16) || !aligned(ws, 4) ||
+        !aligned(y, type_bytes(y_type)))
+        return DGW4_ERR_INVALID_ARG;
+    int8_t *xq = static_cast<int8_t *>(workspace);
+    float *xs = reinterpret_cast<float *>(static_cast<char *>(workspace) + q_bytes);
+    const hipError_t err =
+        dgw4::launch_quantize_rows(x, x_type, T, K, ldx, xq, Kp, xs, (hipStream_t)stream);
+    if (err != hipSuccess)
+        return from_hip(err);
+    const dgw4::I8Args a{xq, xs, wq, ws, T, Kp, N, Kp, ldw, ldy, y, y_type};
+    return from_hip(dgw4::launch_w8a8_linear(a, (hipStream_t)stream));
+}
+
 int dgw4_sample(const float *logits, int R, int V, uint64_t seed, float *entropy, int32_t *sample,
                 int32_t *argmax, void *workspace, size_t *ws_bytes, void *stream)
 {

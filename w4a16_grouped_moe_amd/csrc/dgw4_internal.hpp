@@ -139,6 +139,42 @@ hipError_t launch_read_probe(const void *buf, size_t bytes, uint32_t *sink, hipS
 // floating-point operations.
 hipError_t launch_mfma_probe(int iters, uint32_t *sink, double *flops, hipStream_t stream);
 
+// The layer for few tokens (moe_few.hip): at most kFewMaxAssign assignments.
+constexpr int kFewMaxAssign = 512;
+
+struct FewArgs {
+    const uint16_t *x;          // fp16 [T, d]
+    const int32_t *ids;         // [T, topk]
+    const float *w;             // [T, topk]
+    int T, topk, A, E, d, m;    // A = T * topk
+    const uint8_t *gu_q;        // [E, 2m, d/2]
+    const uint16_t *gu_s, *gu_z;
+    const uint8_t *dn_q;        // [E, d, m/2]
+    const uint16_t *dn_s, *dn_z;
+    int gu_tiled, dn_tiled;
+    uint16_t *h;                // fp16 [A, m], columns permuted per 8 (workspace)
+    uint16_t *out;              // fp16 [T, d]
+};
+
+hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream);
+
+// 8-bit rows and products (int8.hip). Types as DGW4_F32, DGW4_F16, DGW4_BF16.
+hipError_t launch_quantize_rows(const void *x, int type, int rows, int K, long long ldx, int8_t *q,
+                                long long ldq, float *s, hipStream_t stream);
+
+struct I8Args {
+    const int8_t *xq;           // [T, K], rows ldx apart
+    const float *xs;            // [T]
+    const int8_t *wq;           // [N, K], rows ldw apart
+    const float *ws;            // [N]
+    int T, K, N;
+    long long ldx, ldw, ldy;    // in elements
+    void *y;                    // [T, N], rows ldy apart
+    int type;                   // of y
+};
+
+hipError_t launch_w8a8_linear(const I8Args &a, hipStream_t stream);
+
 // y: `halves` (1 or 2) fp16 arrays [T * topk, d] one after the other; each
 // assignment's expert output is their sum.
 hipError_t launch_combine(const uint16_t *y, int halves, const int32_t *topk_ids,
