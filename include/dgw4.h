@@ -426,8 +426,8 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
  *   T >= 0, 1 <= topk <= E, 1 <= E <= 1024, d % gu_g == 0, m % dn_g == 0;
  *   gu_g, dn_g: 64 or 128, each or-ed with DGW4_WEIGHTS_TILED where that
  *   stack is tiled; the DGW4_ROWS_* bits are refused (INVALID_ARG).
- *   T * topk > 512, or x, the intermediate or one expert's weights from
- *   2 GiB: DGW4_ERR_UNSUPPORTED.
+ *   T * topk > 512, d / gu_g > 64, m / dn_g > 32, or x, the intermediate or
+ *   one expert's weights from 2 GiB: DGW4_ERR_UNSUPPORTED.
  * Pointers, alignment (x, the six pack arrays 16 bytes, out 8, workspace
  * 256) and the workspace query (workspace == NULL writes *ws_bytes) as for
  * dgw4_moe_forward; the workspace is this call's own (calls that may overlap

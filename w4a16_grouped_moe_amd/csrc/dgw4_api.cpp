@@ -585,7 +585,8 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
     const long long A = (long long)T * topk;
     // x, the intermediate and one expert's weights are addressed with 32-bit offsets
     if (A > dgw4::kFewMaxAssign || (long long)T * d * 2 >= (1LL << 31) ||
-        A * m * 2 >= (1LL << 31) || (long long)m * d >= (1LL << 31))
+        A * m * 2 >= (1LL << 31) || (long long)m * d >= (1LL << 31) ||
+        d / gu_g > dgw4::kFewMaxUpGroups || m / dn_g > dgw4::kFewMaxDownGroups)
         return DGW4_ERR_UNSUPPORTED;
     const size_t h_bytes = round_up(sizeof(uint16_t) * (size_t)A * (size_t)m);
     const size_t id_bytes = round_up(sizeof(int32_t) * (size_t)A);
@@ -631,10 +632,16 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
     if (routed) {
         int32_t *rids = reinterpret_cast<int32_t *>(ws + h_bytes);
         float *rw = reinterpret_cast<float *>(ws + h_bytes + id_bytes);
-        const hipError_t err =
-            dgw4::launch_router(router_logits, T, E, topk, rids, rw, (hipStream_t)stream);
-        if (err != hipSuccess)
-            return from_hip(err);
+        if (dgw4::few_routes_inside(T, topk, E)) {
+            a.logits = router_logits;
+            a.rids = rids;
+            a.rw = rw;
+        } else {
+            const hipError_t err =
+                dgw4::launch_router(router_logits, T, E, topk, rids, rw, (hipStream_t)stream);
+            if (err != hipSuccess)
+                return from_hip(err);
+        }
         a.ids = rids;
         a.w = rw;
     }

@@ -144,6 +144,9 @@ constexpr int kFewMaxAssign = 512;
 
 struct FewArgs {
     const uint16_t *x;          // fp16 [T, d]
+    const float *logits;        // [T, E]; null: ids and w are given
+    int32_t *rids;              // [T, topk]: where the first launch puts the logits' ids and
+    float *rw;                  //   weights (workspace); ids, w point there then
     const int32_t *ids;         // [T, topk]
     const float *w;             // [T, topk]
     int T, topk, A, E, d, m;    // A = T * topk
@@ -156,6 +159,11 @@ struct FewArgs {
     uint16_t *out;              // fp16 [T, d]
 };
 
+// The groups of d and of m the two kernels keep scales for.
+constexpr int kFewMaxUpGroups = 64, kFewMaxDownGroups = 32;
+
+// Whether launch_few takes a.logits itself; else the router runs before it.
+bool few_routes_inside(int T, int topk, int E);
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream);
 
 // 8-bit rows and products (int8.hip). Types as DGW4_F32, DGW4_F16, DGW4_BF16.

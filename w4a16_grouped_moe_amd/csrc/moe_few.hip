@@ -6,8 +6,9 @@
 //            16) assignments of one tile and splits d over its eight waves.
 //   down     out[t, c] = sum_k w[t, k] (H[a] Wd_e^T)[c], k ascending; a
 //            workgroup takes 16 output columns for every assignment, a wave
-//            one tile at a time, and keeps the experts' outputs in LDS in
-//            fp32 until they are weighted and summed in k order.
+//            one half of m for one tile at a time, and keeps the experts'
+//            outputs in LDS in fp32 until they are weighted and summed in k
+//            order.
 //
 // The layer is bound by the experts' weights, read once each, so both
 // launches split the weights over the whole chip (44 column blocks per expert
@@ -16,48 +17,95 @@
 // that kernel keeps 16 of the 256 compute units busy.
 //
 // A tile is up to 16 assignments of one expert (one MFMA row block). Every
-// workgroup builds the list of tiles itself from the ids (LDS counters and a
-// scan; no launch, no global buffers). All workgroups agree on which
-// assignments a tile holds: an expert with up to 16 has one tile, whose row
-// order is of no matter (each MFMA row is a sum of its own in a fixed order of
-// K); one with more takes its assignments in ascending order, 16 to a tile.
+// workgroup builds the list of tiles itself from the ids (no launch, no
+// global buffers). All workgroups agree on which assignments a tile holds: an
+// expert with up to 16 has one tile, whose row order is of no matter (each
+// MFMA row is a sum of its own in a fixed order of K); one with more takes its
+// assignments in ascending order, 16 to a tile.
 #include "gemm_common.hpp"
+#include "router_keys.hpp"
+
+#include <cmath>
 
 namespace dgw4 {
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / 64;
+constexpr int kUpThreads = 512, kUpWaves = kUpThreads / 64;
+constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / 64;
+constexpr int kSmallAssign = 64;         // assignments that one wave sorts
+constexpr int kFewRouteExperts = 256;    // experts that one wave routes over in registers
 
-// The tile list of one workgroup: s_row[start .. start + n) of tile i are its
-// assignments (low half) with their tokens (high half).
+// Columns of K that one lane-load of packed weights covers are a group G; a
+// wave holds this many groups of weights and activations at once.
+template <int G>
+constexpr int kBatch = G == 128 ? 3 : 6;
+
+// The tile list of one workgroup: tile i holds the assignments row[start ..
+// start + n) (low half, their tokens in the high half).
 struct FewTiles {
-    int count[kMaxExperts];      // assignments of each expert
-    uint32_t base[kMaxExperts];  // first tile << 16 | first row of each expert
-    uint32_t row[kFewMaxAssign];
-    uint32_t tile[kFewMaxAssign];   // expert | start << 10 | rows << 20
-    int32_t id[kFewMaxAssign];   // each assignment's expert, -1 if none
+    uint32_t row[16 * kSmallAssign];
+    uint32_t tile[kFewMaxAssign];        // expert | start << 10 | n << 20
+    int32_t id[kFewMaxAssign];           // each assignment's expert, -1 if none
+    int count[kMaxExperts];              // assignments of each expert
+    uint32_t base[kMaxExperts];          // first tile << 16 | first row of each expert
     int tiles;
 };
+static_assert(16 * kSmallAssign >= kFewMaxAssign, "the row list holds either form");
 
+// A value that every lane of the wave holds, as a scalar.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ inline uint32_t tile_at(const FewTiles &s, int i) { return (uint32_t)uniform((int)s.tile[i]); }
 __device__ inline int tile_expert_of(uint32_t t) { return (int)(t & 0x3FF); }
 __device__ inline int tile_start_of(uint32_t t) { return (int)(t >> 10 & 0x3FF); }
 __device__ inline int tile_rows_of(uint32_t t) { return (int)(t >> 20); }
 
-// ids outside [0, E) belong to no tile.
-__device__ inline void build_tiles(FewTiles &s, const int32_t *__restrict__ ids, int A, int topk, int E)
+// The list from s.id (A entries, written before the last barrier), for up to
+// 64 assignments: lane a of the first wave gathers the mask of the
+// assignments with its expert. 16 row slots per tile.
+__device__ inline void build_tiles_small(FewTiles &s, int A, int topk)
+{
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        const int id = lane < A ? s.id[lane] : -1;
+        uint64_t same = 0;
+        for (int i = 0; i < A; ++i)
+            same |= (uint64_t)(id == __builtin_amdgcn_readlane(id, i)) << i;
+        const bool live = id >= 0;
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        const uint64_t heads = __ballot(live && rank % 16 == 0);
+        // the tile of this lane's rank: its head is the expert's assignment of
+        // rank rank - rank % 16
+        uint64_t m = same;
+        for (int i = 0; i < rank / 16 * 16; ++i)
+            m &= m - 1;
+        const int head = __ffsll((unsigned long long)m) - 1;
+        const int tile = live ? __popcll(heads & ((1ull << head) - 1)) : 0;
+        if (live) {
+            s.row[tile * 16 + rank % 16] = (uint32_t)lane | (uint32_t)(lane / topk) << 16;
+            if (rank % 16 == 0)
+                s.tile[tile] = (uint32_t)id | (uint32_t)(tile * 16) << 10 |
+                               (uint32_t)min(16, __popcll(same) - rank) << 20;
+        }
+        if (lane == 0)
+            s.tiles = __popcll(heads);
+    }
+    __syncthreads();
+}
+
+// The list for any number of assignments: LDS counters and a scan over the
+// experts.
+__device__ inline void build_tiles_any(FewTiles &s, int A, int topk, int E)
 {
     const int tid = threadIdx.x;
     for (int e = tid; e < E; e += blockDim.x)
         s.count[e] = 0;
     __syncthreads();
-    const int id = tid < A ? ids[tid] : -1;
-    const bool live = id >= 0 && id < E;
+    const int id = tid < A ? s.id[tid] : -1;
+    const bool live = id >= 0;
     int rank = 0;
     if (live)
         rank = atomicAdd(&s.count[id], 1);
-    if (tid < A)
-        s.id[tid] = live ? id : -1;
     __syncthreads();
     if (live && s.count[id] > 16) {
         // several tiles: the rank by ascending assignment
@@ -104,168 +152,457 @@ __device__ inline void build_tiles(FewTiles &s, const int32_t *__restrict__ ids,
     __syncthreads();
 }
 
-template <int G, bool TL>
-__global__ void __launch_bounds__(kFewThreads) few_gate_up_kernel(FewArgs a)
+// ids outside [0, E) belong to no tile.
+__device__ inline void build_tiles(FewTiles &s, const int32_t *__restrict__ ids, int A, int topk, int E)
 {
-    __shared__ FewTiles s;
-    __shared__ f32x4 s_red[kFewWaves][2][64];
+    if ((int)threadIdx.x < A) {
+        const int id = ids[threadIdx.x];
+        s.id[threadIdx.x] = id >= 0 && id < E ? id : -1;
+    }
+    __syncthreads();
+    if (A <= kSmallAssign)
+        build_tiles_small(s, A, topk);
+    else
+        build_tiles_any(s, A, topk, E);
+}
+
+// The largest of a wave's values, in every lane: within rows of 16 lanes by
+// DPP shifts, then across the rows by the two row broadcasts.
+__device__ inline uint32_t wave_max(uint32_t v)
+{
+#define DGW4_DPP_MAX(ctrl) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true))
+    DGW4_DPP_MAX(0x111);   // row_shr:1
+    DGW4_DPP_MAX(0x112);   // row_shr:2
+    DGW4_DPP_MAX(0x114);   // row_shr:4
+    DGW4_DPP_MAX(0x118);   // row_shr:8
+    DGW4_DPP_MAX(0x142);   // row_bcast:15
+    DGW4_DPP_MAX(0x143);   // row_bcast:31
+#undef DGW4_DPP_MAX
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// One token's choices by one wave: dgw4_router's ids and weights. Lane l holds
+// the logits of experts l + 64 j; each round takes the largest key (the
+// logit's bits in order, see router_keys.hpp), among equal ones the lowest id.
+__device__ inline void route_token(const float *__restrict__ l, int E, int topk, int32_t *ids_lds,
+                                   int32_t *__restrict__ ids, float *__restrict__ w, bool publish)
+{
+    constexpr int PER = kFewRouteExperts / 64;
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    float v[PER];
+    uint32_t key[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = lane + 64 * j;
+        v[j] = e < E ? l[e] : 0.0f;
+        key[j] = e < E ? order_key(v[j]) : 0u;
+    }
+    float mine = 0.0f;                   // lane k: the k-th choice's logit
+    float top = 0.0f;
+    int id = 0;
+    for (int k = 0; k < topk; ++k) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            best = max(best, key[j]);
+        best = wave_max(best);
+        bool found = false;
+        float lv = 0.0f;
+        int e = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint64_t hit = __ballot(key[j] == best);
+            if (!found && hit) {
+                const int at = __ffsll((unsigned long long)hit) - 1;
+                e = at + 64 * j;
+                lv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v[j]), at));
+                if (lane == at)
+                    key[j] = 0u;
+                found = true;
+            }
+        }
+        if (k == 0)
+            top = lv;
+        if (lane == k) {
+            mine = lv;
+            id = e;
+        }
+    }
+    const float x = lane < topk ? expf(mine - top) : 0.0f;
+    float den = 0.0f;
+    for (int k = 0; k < topk; ++k)
+        den = __fadd_rn(den, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), k)));
+    if (lane < topk) {
+        ids_lds[lane] = id < E ? id : -1;
+        if (publish) {
+            ids[lane] = id;
+            w[lane] = __fdiv_rn(x, den);
+        }
+    }
+}
+
+// gate_up. The (tile, 16 columns) items are dealt to the workgroups in
+// contiguous runs, so a workgroup mostly stays within one tile and keeps its
+// activation fragments in registers from item to item. The eight waves take
+// every eighth group of d; each weight fragment's registers take the next
+// step's load as soon as it has been used. The scales are staged through LDS,
+// one 16-byte load per thread covers the next item's.
+template <int G, bool TL, bool ROUTED, bool MULTI>
+__global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
+{
+    constexpr int NB = kBatch<G>, W = G / 32;
+    __shared__ FewTiles s;
+    __shared__ f32x4 s_red[2][kUpWaves][2][64];
+    extern __shared__ uint4 s_sc[];      // [2][8 * groups]: s and z of the 16 gate, then of the 16 up rows
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = uniform(tid >> 6);
     const int r = lane & 15, p = lane >> 4;
     const int K = a.d;
     const int groups = K / G;
     const int cblocks = a.m / 16;
-    build_tiles(s, a.ids, a.A, a.topk, a.E);
-    const int items = s.tiles * cblocks;
+    if constexpr (ROUTED) {
+        for (int t = wave; t < a.T; t += kUpWaves)
+            route_token(a.logits + (size_t)t * a.E, a.E, a.topk, s.id + t * a.topk, a.rids + t * a.topk,
+                        a.rw + t * a.topk, blockIdx.x == 0);
+        __syncthreads();
+        build_tiles_small(s, a.A, a.topk);
+    } else {
+        build_tiles(s, a.ids, a.A, a.topk, a.E);
+    }
+    const int items = uniform(s.tiles) * cblocks;
+    const int per = items / gridDim.x, rest = items % gridDim.x;
+    int it = (int)blockIdx.x * per + min((int)blockIdx.x, rest);
+    const int end = it + per + ((int)blockIdx.x < rest ? 1 : 0);
+    if (it >= end)
+        return;                          // the whole workgroup: no barrier below is missed
+    const int batches = (groups + kUpWaves * NB - 1) / (kUpWaves * NB);
     const rsrc_t xr = make_rsrc(a.x, (uint32_t)((long long)a.T * K * 2));
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const uint32_t tile = s.tile[it / cblocks];
-        const int cb = it % cblocks;
-        const int n = tile_rows_of(tile);
-        const size_t e = (size_t)tile_expert_of(tile);
-        const rsrc_t wr = make_rsrc(a.gu_q + e * (size_t)a.m * K, (uint32_t)a.m * (uint32_t)K);
-        const uint16_t *sp = a.gu_s + (e * 2 * a.m + cb * 16 + r) * (size_t)groups;
-        const uint16_t *zp = a.gu_z + (e * 2 * a.m + cb * 16 + r) * (size_t)groups;
-        const size_t up_off = (size_t)a.m * groups;
-        const uint32_t wg = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
-        const uint32_t wu = wq_lane_off<G, TL>(a.m + cb * 16 + r, lane, K);
-        const uint32_t xrow = r < n ? (s.row[tile_start_of(tile) + r] >> 16) * (uint32_t)(K * 2) +
-                                          (uint32_t)(p * (G / 2))
-                                    : kOutOfRange;
-        f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        for (int gi = wave; gi < groups; gi += kFewWaves) {
-            Frag<G> w[2];
-            w[0] = load_frag<G, false>(wr, wg + wq_group_off<G, TL>(gi), 0);
-            w[1] = load_frag<G, false>(wr, wu + wq_group_off<G, TL>(gi), 0);
-            uint4 xv[G / 32];
+    const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows
+
+    auto load_scales = [&](int item) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (item < end && tid < 4 * n_sc) {
+            const uint32_t tile = tile_at(s, item / cblocks);
+            const int part = tid / n_sc, i = tid - part * n_sc;
+            const size_t row = (size_t)tile_expert_of(tile) * 2 * a.m + (part >= 2 ? a.m : 0) +
+                               (item % cblocks) * 16;
+            const uint16_t *src = (part & 1) ? a.gu_z : a.gu_s;
+            v = reinterpret_cast<const uint4 *>(src + row * groups)[i];
+        }
+        return v;
+    };
+    // one step's weight loads: its resource and lane offsets, then one load per
+    // group and half
+    struct Source {
+        rsrc_t rsrc;
+        uint32_t lane[2];
+        int b;
+        bool live;
+    };
+    auto source = [&](int item, int b) {
+        const int i = min(item, end - 1);
+        const int c0 = (i % cblocks) * 16;
+        Source q;
+        q.rsrc = make_rsrc(a.gu_q + (size_t)tile_expert_of(tile_at(s, i / cblocks)) * a.m * K,
+                           (uint32_t)a.m * (uint32_t)K);
+        q.lane[0] = wq_lane_off<G, TL>(c0 + r, lane, K);
+        q.lane[1] = wq_lane_off<G, TL>(a.m + c0 + r, lane, K);
+        q.b = b;
+        q.live = item < end;
+        return q;
+    };
+    auto load_weight = [&](const Source &q, int h, int j) {
+        const int gi = wave + kUpWaves * (q.b * NB + j);
+        return load_frag<G, TL>(q.rsrc, gi < groups && q.live ? q.lane[h] + wq_group_off<G, TL>(gi) : kOutOfRange, 0);
+    };
+
+    uint4 sc = load_scales(it);
+    Frag<G> w[2][NB];
+    {
+        const Source q = source(it, 0);
 #pragma unroll
-            for (int t = 0; t < G / 32; ++t)
-                xv[t] = load16(xr, xrow == kOutOfRange ? kOutOfRange : xrow + (uint32_t)(gi * G * 2 + t * 16), 0);
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[h][j] = load_weight(q, h, j);
+    }
+    if (tid < 4 * n_sc)
+        s_sc[tid] = sc;
+    __syncthreads();
+    uint4 xv[NB][W];
+    int have = -1, buf = 0;
+    f32x4 acc[2];
+    for (int b = 0; it < end;) {
+        const uint32_t tile = tile_at(s, it / cblocks);
+        const int n = tile_rows_of(tile), start = tile_start_of(tile);
+        if (have != (it / cblocks) * batches + b) {
+            have = (it / cblocks) * batches + b;
+            const uint32_t xrow = r < n ? (s.row[start + r] >> 16) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2))
+                                        : kOutOfRange;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int gi = wave + kUpWaves * (b * NB + j);
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    xv[j][t] = load16(xr, r < n && gi < groups ? xrow + (uint32_t)(gi * G * 2 + t * 16)
+                                                               : kOutOfRange, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    xv[j][t] = permute8(xv[j][t]);
+        }
+        const bool last = !MULTI || b == batches - 1;
+        const int nit = last ? it + 1 : it, nb = last ? 0 : b + 1;
+        if (!MULTI || b == 0) {
+            sc = load_scales(it + 1);
+            acc[0] = acc[1] = f32x4{0, 0, 0, 0};
+        }
+        const Source q = source(nit, nb);
+        const uint16_t *sl = reinterpret_cast<const uint16_t *>(s_sc + buf * 4 * n_sc) + r * groups;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int gi = min(wave + kUpWaves * (b * NB + j), groups - 1);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 f16x2 c1024, c64;
-                zero_point_consts(zp[h * up_off + gi], c1024, c64);
-                const float sc = (float)__builtin_bit_cast(_Float16, sp[h * up_off + gi]);
+                zero_point_consts(sl[(2 * h + 1) * 16 * groups + gi], c1024, c64);
+                // past the last group: x is zero there, and the scale a finite one
+                const float sv = (float)__builtin_bit_cast(_Float16, sl[2 * h * 16 * groups + gi]);
                 f32x4 part = {0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < G / 32; ++t)
+                for (int t = 0; t < W; ++t)
                     part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        __builtin_bit_cast(f16x8, permute8(xv[t])),
-                        dequant8(frag_word<G>(w[h], t), c1024, c64), part, 0, 0, 0);
-                acc[h] += sc * part;
+                        __builtin_bit_cast(f16x8, xv[j][t]), dequant8(frag_word<G>(w[h][j], t), c1024, c64),
+                        part, 0, 0, 0);
+                acc[h] += sv * part;
+                w[h][j] = load_weight(q, h, j);        // the next step's, into the registers just read
             }
         }
-        s_red[wave][0][lane] = acc[0];
-        s_red[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            const int i = threadIdx.x >> 4, c = threadIdx.x & 15;   // tile row, column
+        if (last) {
+            s_red[buf][wave][0][lane] = acc[0];
+            s_red[buf][wave][1][lane] = acc[1];
+            if (tid < 4 * n_sc)
+                s_sc[(buf ^ 1) * 4 * n_sc + tid] = sc;
+            __syncthreads();
+            const int i = tid >> 4, c = tid & 15;      // tile row, column
             if (i < n) {
                 const int src = (i >> 2) * 16 + c;
                 float g = 0.f, u = 0.f;
 #pragma unroll
-                for (int v = 0; v < kFewWaves; ++v) {
-                    g += s_red[v][0][src][i & 3];
-                    u += s_red[v][1][src][i & 3];
+                for (int v = 0; v < kUpWaves; ++v) {
+                    g += s_red[buf][v][0][src][i & 3];
+                    u += s_red[buf][v][1][src][i & 3];
                 }
-                const uint32_t at = s.row[tile_start_of(tile) + i] & 0xFFFF;
+                const uint32_t at = s.row[start + i] & 0xFFFF;
                 const _Float16 hv = (_Float16)(gelu_tanh(g) * u);
-                a.h[(size_t)at * a.m + permuted_col(cb * 16 + c)] = __builtin_bit_cast(uint16_t, hv);
+                a.h[(size_t)at * a.m + permuted_col((it % cblocks) * 16 + c)] = __builtin_bit_cast(uint16_t, hv);
             }
+            buf ^= 1;
         }
-        __syncthreads();
+        it = nit;
+        b = nb;
     }
 }
 
-template <int G, bool TL>
-__global__ void __launch_bounds__(kFewThreads) few_down_kernel(FewArgs a)
+// down and the weighted sum. A unit is one half of m's groups for one tile;
+// a wave takes every sixteenth unit, with the next step's weights loaded into
+// each fragment's registers as soon as it has been used (MULTI: the half holds
+// more than one step's groups). The scales of the tile's 16 rows are contiguous:
+// one 16-byte load per lane (NS of them past 16 groups) into the wave's own
+// slot of LDS.
+template <int G, bool TL, int NS, bool MULTI>
+__global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
+    constexpr int NB = kBatch<G>, W = G / 32;
     __shared__ FewTiles s;
-    extern __shared__ float s_y[];     // [A][16]
+    __shared__ float s_w[kFewMaxAssign];
+    extern __shared__ uint4 s_dyn[];     // scales [waves][64 * NS], then Y [2][A][16] fp32
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = uniform((int)threadIdx.x >> 6);
     const int r = lane & 15, p = lane >> 4;
     const int K = a.m;
     const int groups = K / G;
     const int cb = blockIdx.x;
+    uint4 *sc_lds = s_dyn + wave * 64 * NS;
+    float *s_y = reinterpret_cast<float *>(s_dyn + kDownWaves * 64 * NS);
+    if ((int)threadIdx.x < a.A)
+        s_w[threadIdx.x] = a.w[threadIdx.x];
     build_tiles(s, a.ids, a.A, a.topk, a.E);
     const rsrc_t hr = make_rsrc(a.h, (uint32_t)((long long)a.A * K * 2));
-    for (int it = wave; it < s.tiles; it += kFewWaves) {
-        const uint32_t tile = s.tile[it];
-        const int n = tile_rows_of(tile);
-        const int start = tile_start_of(tile);
-        const size_t e = (size_t)tile_expert_of(tile);
-        const rsrc_t wr = make_rsrc(a.dn_q + e * (size_t)a.d * (K / 2), (uint32_t)a.d * (uint32_t)(K / 2));
-        const uint16_t *sp = a.dn_s + (e * a.d + cb * 16 + r) * (size_t)groups;
-        const uint16_t *zp = a.dn_z + (e * a.d + cb * 16 + r) * (size_t)groups;
-        const uint32_t wo = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
-        const uint32_t hrow = r < n ? (s.row[start + r] & 0xFFFF) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2))
-                                    : kOutOfRange;
-        f32x4 acc = {0, 0, 0, 0};
-        for (int gi = 0; gi < groups; ++gi) {
-            const Frag<G> w = load_frag<G, false>(wr, wo + wq_group_off<G, TL>(gi), 0);
-            uint4 hv[G / 32];
+    const int half_groups = (groups + 1) / 2;
+    const int batches = (half_groups + NB - 1) / NB;
+    const int units = uniform(s.tiles) * 2;
+    const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows (z's follow from 32 NS)
+
+    auto load_scales = [&](uint4 (&v)[NS], int unit) {
+        const size_t row = (size_t)tile_expert_of(tile_at(s, min(unit, units - 1) >> 1)) * a.d + cb * 16;
+        const uint16_t *sp = a.dn_s + row * groups, *zp = a.dn_z + row * groups;
 #pragma unroll
-            for (int t = 0; t < G / 32; ++t)
-                hv[t] = load16(hr, hrow == kOutOfRange ? kOutOfRange : hrow + (uint32_t)(gi * G * 2 + t * 16), 0);
-            f16x2 c1024, c64;
-            zero_point_consts(zp[gi], c1024, c64);
-            const float sc = (float)__builtin_bit_cast(_Float16, sp[gi]);
-            f32x4 part = {0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < G / 32; ++t)
-                part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    __builtin_bit_cast(f16x8, hv[t]), dequant8(frag_word<G>(w, t), c1024, c64), part,
-                    0, 0, 0);
-            acc += sc * part;
+        for (int i = 0; i < NS; ++i) {
+            const int at = lane + 64 * i;
+            const bool z = at >= 32 * NS;
+            v[i] = reinterpret_cast<const uint4 *>(z ? zp : sp)[min(z ? at - 32 * NS : at, n_sc - 1)];
         }
+    };
+    struct Source {
+        rsrc_t rsrc;
+        uint32_t lane;
+        int g0, g1;
+    };
+    // the groups of one step and where its weights are; none past the last unit
+    auto source = [&](int unit, int b) {
+        const int u = min(unit, units - 1);
+        Source q;
+        q.rsrc = make_rsrc(a.dn_q + (size_t)tile_expert_of(tile_at(s, u >> 1)) * a.d * (K / 2),
+                           (uint32_t)a.d * (uint32_t)(K / 2));
+        q.lane = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
+        q.g1 = unit < units ? ((u & 1) ? groups : half_groups) : 0;
+        q.g0 = (u & 1) * half_groups + b * NB;
+        return q;
+    };
+    auto load_weight = [&](const Source &q, int j) {
+        const int gi = q.g0 + j;
+        return load_frag<G, TL>(q.rsrc, gi < q.g1 ? q.lane + wq_group_off<G, TL>(gi) : kOutOfRange, 0);
+    };
+
+    if (wave < units) {
+        uint4 sc[NS];
+        Frag<G> w[NB];
+        load_scales(sc, wave);
+        Source cur = source(wave, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (4 * p + i < n)
-                s_y[(s.row[start + 4 * p + i] & 0xFFFF) * 16 + r] = acc[i];
+        for (int j = 0; j < NB; ++j)
+            w[j] = load_weight(cur, j);
+        f32x4 acc = {0, 0, 0, 0};
+        for (int u = wave, b = 0; u < units;) {
+            const uint32_t tile = tile_at(s, u >> 1);
+            const int n = tile_rows_of(tile), start = tile_start_of(tile);
+            const uint32_t hrow = (s.row[start + min(r, n - 1)] & 0xFFFF) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2));
+            uint4 hv[NB][W];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    hv[j][t] = load16(hr, r < n && cur.g0 + j < cur.g1
+                                              ? hrow + (uint32_t)((cur.g0 + j) * G * 2 + t * 16) : kOutOfRange, 0);
+            const bool last = !MULTI || b == batches - 1;
+            const int nu = last ? u + kDownWaves : u, nb = last ? 0 : b + 1;
+            if (!MULTI || b == 0) {
+                // the wave's own LDS slot: its earlier reads are done, in order
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    sc_lds[lane + 64 * i] = sc[i];
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                load_scales(sc, u + kDownWaves);
+                acc = f32x4{0, 0, 0, 0};
+            }
+            const Source next = source(nu, nb);
+            const uint16_t *sl = reinterpret_cast<const uint16_t *>(sc_lds) + r * groups;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                // past the last group: h is zero there, and the scale a finite one
+                const int gi = min(cur.g0 + j, groups - 1);
+                f16x2 c1024, c64;
+                zero_point_consts(sl[32 * NS * 8 + gi], c1024, c64);
+                const float sv = (float)__builtin_bit_cast(_Float16, sl[gi]);
+                f32x4 part = {0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        __builtin_bit_cast(f16x8, hv[j][t]), dequant8(frag_word<G>(w[j], t), c1024, c64),
+                        part, 0, 0, 0);
+                acc += sv * part;
+                w[j] = load_weight(next, j);       // the next step's, into the registers just read
+            }
+            if (last) {
+                float *y = s_y + (u & 1) * a.A * 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * p + i < n)
+                        y[(s.row[start + 4 * p + i] & 0xFFFF) * 16 + r] = acc[i];
+                __builtin_amdgcn_wave_barrier();
+            }
+            u = nu;
+            b = nb;
+            cur = next;
+        }
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < a.T * 16; o += blockDim.x) {
+    for (int o = threadIdx.x; o < a.T * 16; o += kDownThreads) {
         const int t = o >> 4, c = o & 15;
         float v = 0.f;
         for (int k = 0; k < a.topk; ++k) {
-            const int id = a.ids[t * a.topk + k];
-            if (id >= 0 && id < a.E)
-                v = __fadd_rn(v, __fmul_rn(a.w[t * a.topk + k], s_y[(t * a.topk + k) * 16 + c]));
+            const int at = t * a.topk + k;
+            if (s.id[at] >= 0)
+                v = __fadd_rn(v, __fmul_rn(s_w[at], __fadd_rn(s_y[at * 16 + c], s_y[(a.A + at) * 16 + c])));
         }
         a.out[(size_t)t * a.d + cb * 16 + c] = __builtin_bit_cast(uint16_t, (_Float16)v);
     }
 }
 
 template <int G, bool TL>
-hipError_t run_gate_up(const FewArgs &a, hipStream_t st)
+hipError_t run_gate_up(const FewArgs &a, bool routed, hipStream_t st)
 {
     const int items = a.A * (a.m / 16);
-    few_gate_up_kernel<G, TL><<<dim3(items < 512 ? items : 512), dim3(kFewThreads), 0, st>>>(a);
+    const size_t lds = 2 * 8 * (size_t)(a.d / G) * 16;
+    const dim3 grid(items < 512 ? items : 512), block(kUpThreads);
+    const bool multi = a.d / G > kUpWaves * kBatch<G>;
+    if (routed && multi)
+        few_gate_up_kernel<G, TL, true, true><<<grid, block, lds, st>>>(a);
+    else if (routed)
+        few_gate_up_kernel<G, TL, true, false><<<grid, block, lds, st>>>(a);
+    else if (multi)
+        few_gate_up_kernel<G, TL, false, true><<<grid, block, lds, st>>>(a);
+    else
+        few_gate_up_kernel<G, TL, false, false><<<grid, block, lds, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int G, bool TL, int NS, bool MULTI>
+hipError_t run_down(const FewArgs &a, hipStream_t st)
+{
+    static size_t allowed = 32 * 1024;
+    const size_t lds = (size_t)kDownWaves * 64 * NS * 16 + (size_t)a.A * 2 * 64;
+    const hipError_t err = allow_lds(few_down_kernel<G, TL, NS, MULTI>, lds, allowed);
+    if (err != hipSuccess)
+        return err;
+    few_down_kernel<G, TL, NS, MULTI><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
     return hipGetLastError();
 }
 
 template <int G, bool TL>
-hipError_t run_down(const FewArgs &a, hipStream_t st)
+hipError_t pick_down(const FewArgs &a, hipStream_t st)
 {
-    few_down_kernel<G, TL><<<dim3(a.d / 16), dim3(kFewThreads), (size_t)a.A * 64, st>>>(a);
-    return hipGetLastError();
+    const int groups = a.m / G;
+    if (groups <= 2 * kBatch<G>)
+        return run_down<G, TL, 1, false>(a, st);
+    return groups <= 16 ? run_down<G, TL, 1, true>(a, st) : run_down<G, TL, 2, true>(a, st);
 }
 
 }  // namespace
 
+bool few_routes_inside(int T, int topk, int E)
+{
+    return T * topk <= kSmallAssign && E <= kFewRouteExperts;
+}
+
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream)
 {
     hipError_t err;
+    const bool routed = a.logits != nullptr;
     if (gu_g == 128)
-        err = a.gu_tiled ? run_gate_up<128, true>(a, stream) : run_gate_up<128, false>(a, stream);
+        err = a.gu_tiled ? run_gate_up<128, true>(a, routed, stream) : run_gate_up<128, false>(a, routed, stream);
     else
-        err = a.gu_tiled ? run_gate_up<64, true>(a, stream) : run_gate_up<64, false>(a, stream);
+        err = a.gu_tiled ? run_gate_up<64, true>(a, routed, stream) : run_gate_up<64, false>(a, routed, stream);
     if (err != hipSuccess)
         return err;
     if (dn_g == 128)
-        return a.dn_tiled ? run_down<128, true>(a, stream) : run_down<128, false>(a, stream);
-    return a.dn_tiled ? run_down<64, true>(a, stream) : run_down<64, false>(a, stream);
+        return a.dn_tiled ? pick_down<128, true>(a, stream) : pick_down<128, false>(a, stream);
+    return a.dn_tiled ? pick_down<64, true>(a, stream) : pick_down<64, false>(a, stream);
 }
 
 }  // namespace dgw4

@@ -21,7 +21,7 @@
 // "larger logit, or equal logit at a lower id" for finite logits. The
 // weights' exp terms are laid out in choice order and summed in that order
 // by every lane.
-#include "dgw4_internal.hpp"
+#include "router_keys.hpp"
 
 #include <cmath>
 
@@ -30,17 +30,11 @@ namespace {
 
 constexpr int kRouterWaves = 4;                  // tokens per workgroup
 
-// The ranking key of logit v of expert e: a larger key ranks first. The
-// float's bits become an unsigned integer in the floats' order (negative
-// values complemented, non-negative ones with the top bit set; -0 as +0),
-// the id's complement below it puts equal logits in ascending id order.
+// The ranking key of logit v of expert e: a larger key ranks first. The id's
+// complement below the logit's order puts equal logits in ascending id order.
 __device__ inline uint64_t rank_key(float v, int e)
 {
-    uint32_t b = __builtin_bit_cast(uint32_t, v);
-    if (b == 0x80000000u)
-        b = 0u;
-    const uint32_t u = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return (uint64_t)u << 32 | (uint32_t)~e;
+    return (uint64_t)order_key(v) << 32 | (uint32_t)~e;
 }
 
 template <int PER>
