@@ -183,6 +183,23 @@ struct I8Args {
 
 hipError_t launch_w8a8_linear(const I8Args &a, hipStream_t stream);
 
+// The product for few tokens (int8_few.hip): up to kI8FewTokens whose codes fit
+// LDS, from codes (x_type kI8Codes) or from activations x of x_type [T, k_x],
+// rows ld apart (g.xq and g.xs unused, g.K = k_x in whole 16s).
+constexpr int kI8FewTokens = 32;
+constexpr int kI8FewWideN = 65536;
+constexpr int kI8Codes = -1;
+
+struct I8FewArgs {
+    I8Args g;
+    const void *x;
+    int x_type, k_x;
+    long long ld;
+};
+
+bool i8_few_fits(int T, int K);
+hipError_t launch_i8_few(const I8FewArgs &a, hipStream_t stream);
+
 // y: `halves` (1 or 2) fp16 arrays [T * topk, d] one after the other; each
 // assignment's expert output is their sum.
 hipError_t launch_combine(const uint16_t *y, int halves, const int32_t *topk_ids,

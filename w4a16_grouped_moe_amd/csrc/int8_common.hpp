@@ -1,0 +1,80 @@
+// Device helpers of the 8-bit sources (not part of the ABI).
+#pragma once
+
+#include "gemm_common.hpp"
+
+#include "dgw4.h"
+
+namespace dgw4 {
+namespace {
+
+// every rounding of the 8-bit entry points is stated in the header: no product
+// is folded into a sum or a conversion
+#pragma clang fp contract(off)
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ inline float to_f32(float v) { return v; }
+__device__ inline float to_f32(_Float16 v) { return (float)v; }
+__device__ inline float to_f32(__bf16 v)
+{
+    return __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(uint16_t, v) << 16);
+}
+
+// v rounded to Ty. The empty asm keeps the fp32 rounding of the product before
+// it: the compiler would otherwise form the product and its fp16 rounding in
+// one v_fma_mixlo_f16.
+template <class Ty>
+__device__ inline Ty from_f32(float v)
+{
+    asm("" : "+v"(v));
+    return (Ty)v;
+}
+
+// One output: the integer sum, rounded to fp32, times the token's scale, times
+// the channel's, each product rounded, then rounded to Ty.
+template <class Ty>
+__device__ inline Ty scaled(int acc, float xs, float ws)
+{
+    return from_f32<Ty>(__fmul_rn(__fmul_rn((float)acc, xs), ws));
+}
+
+// Four neighbouring outputs of a row, channels c .. c + 3 of N: one store where
+// the row allows it (vec: y and ldy in whole fours), element stores else.
+template <class Ty>
+__device__ inline void store4(Ty *row, int c, int N, bool vec, i32x4 acc, float xs, f32x4 ws)
+{
+    typedef Ty ty4 __attribute__((ext_vector_type(4)));
+    if (vec && c + 3 < N) {
+        ty4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = scaled<Ty>(acc[i], xs, ws[i]);
+        *reinterpret_cast<ty4 *>(row + c) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < N)
+                row[c + i] = scaled<Ty>(acc[i], xs, ws[i]);
+    }
+}
+
+// Whether rows of y may be stored four elements at a time.
+template <class Ty>
+__device__ inline bool rows_in_fours(const I8Args &a)
+{
+    return a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(Ty))) == 0;
+}
+
+// The scales of channels c .. c + 3 (0 past N).
+__device__ inline f32x4 channel_scales(const I8Args &a, int c)
+{
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = c + i < a.N ? a.ws[c + i] : 0.0f;
+    return v;
+}
+
+}  // namespace
+}  // namespace dgw4

@@ -1,0 +1,210 @@
+// Products of 8-bit rows over many tokens, y[t, n] = xs[t] ws[n] sum_k xq wq,
+// in LDS tiles.
+//
+// A workgroup takes BN channels x BT tokens and walks K in stages of 128
+// bytes, ST stages deep in LDS. A stage's rows (BN of W, then BT of X, 128
+// bytes each, whole cache lines) are copied from global memory straight into
+// LDS, 16 bytes a lane, without passing through registers; one barrier per
+// stage. Position c of a row's eight 16-byte pieces holds piece c ^ (row % 8),
+// chosen by the lane that loads it, so that the 16 rows one MFMA fragment
+// reads at the same K fall on all banks. A lane's offset past K reads as zero
+// (buffer bounds), and rows past T or N repeat the last row, their outputs not
+// stored.
+//
+// v_mfma_i32_16x16x64_i8 takes the channels as its row operand: a lane ends
+// with four consecutive channels of one token. The sums are exact, so their
+// order is of no matter.
+#include "int8_common.hpp"
+
+#include <cmath>
+#include <stdlib.h>
+
+namespace dgw4 {
+namespace {
+
+constexpr int kStageK = 128;                     // bytes of K per stage
+constexpr uint32_t kPast = 0x80000000u;          // an offset past every buffer here
+
+// 64 lanes x 16 bytes from the buffer into LDS at lds (wave-uniform), lane
+// after lane. No register receives the data; the caller waits on vmcnt.
+__device__ inline void copy_to_lds(rsrc_t r, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(r)
+                 : "memory");
+}
+
+// All of this wave's LDS reads have returned and at most N of its copies are
+// still in flight; then the workgroup's barrier.
+template <int N>
+__device__ inline void stage_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+template <int BN, int BT, int WN, int WT, int ST, class Ty>
+__global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8Args a, int tiles_n, int tiles_t)
+{
+    constexpr int kWaves = (BN / WN) * (BT / WT);
+    constexpr int kLoadsW = BN / 8 / kWaves, kLoadsX = BT / 8 / kWaves;   // copies per wave and stage, 8 rows each
+    constexpr int kLoads = kLoadsW + kLoadsX;
+    constexpr int kStage = (BN + BT) * kStageK;
+    constexpr int NA = WN / 16, NB = WT / 16;
+    static_assert(BN % (8 * kWaves) == 0 && BT % (8 * kWaves) == 0, "whole copies for each wave");
+    extern __shared__ char s_mem[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int r = lane & 15, p = lane >> 4;
+
+    // workgroup -> tile: an XCD (workgroups i, i + 8, ...) takes a contiguous run
+    // of tiles, in groups of 8 token tiles so that the tiles in flight share
+    // both their weights and their tokens in the XCD's L2
+    const int total = tiles_n * tiles_t;
+    const int per = total / kXcds, rest = total % kXcds;
+    const int x = blockIdx.x % kXcds, i0 = blockIdx.x / kXcds;
+    const int id = x * per + min(x, rest) + i0;
+    const int group = id / (8 * tiles_n);
+    const int gt = min(8, tiles_t - group * 8);
+    const int in = id - group * 8 * tiles_n;
+    const int n0 = in / gt * BN, t0 = (group * 8 + in % gt) * BT;
+
+    // this wave's copies: 8 rows each of W, then of X
+    const int rows_w = min(BN, a.N - n0), rows_x = min(BT, a.T - t0);
+    const rsrc_t rw = make_rsrc(a.wq + (size_t)n0 * a.ldw, (uint32_t)(rows_w - 1) * (uint32_t)a.ldw + (uint32_t)a.K);
+    const rsrc_t rx = make_rsrc(a.xq + (size_t)t0 * a.ldx, (uint32_t)(rows_x - 1) * (uint32_t)a.ldx + (uint32_t)a.K);
+    const uint32_t kl = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);      // this lane's piece of K
+    uint32_t off[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        off[i] = i < kLoadsW
+                     ? (uint32_t)min((wave * kLoadsW + i) * 8 + (lane >> 3), rows_w - 1) * (uint32_t)a.ldw + kl
+                     : (uint32_t)min((wave * kLoadsX + i - kLoadsW) * 8 + (lane >> 3), rows_x - 1) * (uint32_t)a.ldx + kl;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)s_mem;
+    const uint32_t lds_w = lds0 + (uint32_t)(wave * kLoadsW * 1024);
+    const uint32_t lds_x = lds0 + (uint32_t)(BN * kStageK + wave * kLoadsX * 1024);
+
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    auto issue = [&](int st, int buf) {
+        const uint32_t k0 = (uint32_t)st * kStageK;
+        const bool in_k = k0 + kl < (uint32_t)a.K;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            copy_to_lds(i < kLoadsW ? rw : rx, in_k ? off[i] + k0 : kPast,
+                        (i < kLoadsW ? lds_w + (uint32_t)(i * 1024) : lds_x + (uint32_t)((i - kLoadsW) * 1024)) +
+                            (uint32_t)(buf * kStage));
+    };
+
+    i32x4 acc[NA][NB];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+
+    const int wn = wave % (BN / WN) * WN, wt = wave / (BN / WN) * WT;
+    const uint32_t fa = (uint32_t)((wn + r) * kStageK + (p ^ (r & 7)) * 16);
+    const uint32_t fb = fa + (uint32_t)((BN + wt - wn) * kStageK);
+#pragma unroll
+    for (int st = 0; st < ST - 1; ++st)
+        issue(st, st);
+    int buf = 0, nbuf = ST - 1;
+    for (int st = 0; st < stages; ++st) {
+        stage_barrier<kLoads * (ST - 2)>();
+        issue(st + ST - 1, nbuf);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x4 fw[NA], fx[NB];
+            // piece 4 kk + p of the row: the two halves' positions differ in bit 2
+            const char *ra = s_mem + ((fa + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
+            const char *rb = s_mem + ((fb + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+                fw[i] = *reinterpret_cast<const i32x4 *>(ra + i * 16 * kStageK);
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                fx[j] = *reinterpret_cast<const i32x4 *>(rb + j * 16 * kStageK);
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], fx[j], acc[i][j], 0, 0, 0);
+        }
+        buf = buf + 1 == ST ? 0 : buf + 1;
+        nbuf = nbuf + 1 == ST ? 0 : nbuf + 1;
+    }
+    stage_barrier<0>();                  // no copy may still land when the workgroup ends
+
+    const bool vec = rows_in_fours<Ty>(a);
+    f32x4 ws[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+        ws[i] = channel_scales(a, n0 + wn + i * 16 + 4 * p);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const int t = t0 + wt + j * 16 + r;
+        if (t < a.T) {
+            const float xs = a.xs[t];
+            Ty *y = (Ty *)a.y + (size_t)t * a.ldy;
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+                store4<Ty>(y, n0 + wn + i * 16 + 4 * p, a.N, vec, acc[i][j], xs, ws[i]);
+        }
+    }
+}
+
+template <int BN, int BT, int WN, int WT, int ST, class Ty>
+hipError_t run(const I8Args &a, hipStream_t st)
+{
+    static size_t allowed = 64 * 1024;
+    constexpr size_t lds = (size_t)ST * (BN + BT) * kStageK;
+    const hipError_t err = allow_lds(i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>, lds, allowed);
+    if (err != hipSuccess)
+        return err;
+    const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
+    i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>
+        <<<dim3(tn * tt), dim3((BN / WN) * (BT / WT) * 64), lds, st>>>(a, tn, tt);
+    return hipGetLastError();
+}
+
+// The tile by the least estimated time: rounds of workgroups over the chip
+// times a round's time, measured at K = 2816 (22 stages; all scale with K).
+// 256 x 256 and 256 x 128 tiles fill a CU alone; the small ones share it and
+// are then bound by their rate (us per tile and CU) rather than a round.
+//   256 x 256: 42 us a round    256 x 128: 27    128 x 128: 17
+//   64 x 64: 9.0, or 6.5 per tile and CU    64 x 32: 7.5, or 4.1
+// At T = 512, N = 2816: 40.2 / 24.8 / 16.5 / 12.1 / 13.3 us measured; at T = 512,
+// N = 32768: 52.2 / 59.7 / 77.8 / 104 / 130.
+template <class Ty>
+hipError_t pick(const I8Args &a, hipStream_t st)
+{
+    auto tiles = [&](int bn, int bt) {
+        return (double)((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt) / 256.0;
+    };
+    const double est[5] = {42.0 * ceil(tiles(256, 256)), 27.0 * ceil(tiles(256, 128)), 17.0 * ceil(tiles(128, 128)),
+                           fmax(9.0, 6.5 * tiles(64, 64)), fmax(7.5, 4.1 * tiles(64, 32))};
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+        if (est[i] < est[best])
+            best = i;
+    const char *e = getenv("DGW4_FORCE");
+    if (e) best = atoi(e);
+    switch (best) {
+    case 0: return run<256, 256, 64, 128, 2, Ty>(a, st);
+    case 1: return run<256, 128, 64, 64, 3, Ty>(a, st);
+    case 2: return run<128, 128, 64, 32, 4, Ty>(a, st);
+    case 3: return run<64, 64, 32, 32, 4, Ty>(a, st);
+    default: return run<64, 32, 32, 16, 4, Ty>(a, st);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_w8a8_linear(const I8Args &a, hipStream_t stream)
+{
+    return a.type == DGW4_F32 ? pick<float>(a, stream)
+           : a.type == DGW4_F16 ? pick<_Float16>(a, stream)
+                                : pick<__bf16>(a, stream);
+}
+
+}  // namespace dgw4
