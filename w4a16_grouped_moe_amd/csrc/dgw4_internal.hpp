@@ -187,7 +187,9 @@ hipError_t launch_w8a8_linear(const I8Args &a, hipStream_t stream);
 // LDS, from codes (x_type kI8Codes) or from activations x of x_type [T, k_x],
 // rows ld apart (g.xq and g.xs unused, g.K = k_x in whole 16s).
 constexpr int kI8FewTokens = 32;
-constexpr int kI8FewWideN = 65536;
+// Tokens quantised inside the product's launch: every workgroup does all of
+// them (about 0.6 us a token at K = 2816), a launch before it costs 3.6 us.
+constexpr int kI8FewQuantised = 6;
 constexpr int kI8Codes = -1;
 
 struct I8FewArgs {
@@ -195,10 +197,12 @@ struct I8FewArgs {
     const void *x;
     int x_type, k_x;
     long long ld;
+    uint32_t row_magic;         // set by launch_i8_few, as is run
+    int run;                    // neighbouring blocks of 16 channels a workgroup takes in turn
 };
 
 bool i8_few_fits(int T, int K);
-hipError_t launch_i8_few(const I8FewArgs &a, hipStream_t stream);
+hipError_t launch_i8_few(I8FewArgs a, hipStream_t stream);
 
 // y: `halves` (1 or 2) fp16 arrays [T * topk, d] one after the other; each
 // assignment's expert output is their sum.

@@ -76,5 +76,31 @@ __device__ inline f32x4 channel_scales(const I8Args &a, int c)
     return v;
 }
 
+constexpr uint32_t kPast = 0x80000000u;          // an offset past every buffer here
+
+// 64 lanes x 16 bytes from the buffer into LDS at lds (wave-uniform), lane
+// after lane. No register receives the data; the caller waits on vmcnt.
+__device__ inline void copy_to_lds(rsrc_t r, uint32_t voff, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(r)
+                 : "memory");
+}
+
+// All of this wave's LDS reads have returned and at most N of its copies are
+// still in flight; then the workgroup's barrier.
+template <int N>
+__device__ inline void stage_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// A pointer into LDS as the byte offset that copies take.
+__device__ inline uint32_t lds_offset(const void *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
 }  // namespace
 }  // namespace dgw4

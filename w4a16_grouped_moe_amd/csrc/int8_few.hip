@@ -4,15 +4,18 @@
 // The weights, read once, are all the work. The tokens' codes lie in LDS
 // (quantised there from the activations, or copied), rows 16 bytes off the
 // bank period so that the 16 rows of an MFMA fragment fall on all banks, zero
-// past K. A wave holds six fragments of weights (16 channels x 64 bytes) and
-// refills each as soon as it has been used; v_mfma_i32_16x16x64_i8 takes the
-// channels as its row operand.
+// past K. A workgroup takes 16 channels at a time, its eight waves every
+// eighth 128 bytes of K each; a wave holds six fragments of weights (16
+// channels x 64 bytes) and refills each with the next step's as soon as it has
+// been used. v_mfma_i32_16x16x64_i8 takes the channels as its row operand; the
+// waves' sums meet in LDS (integers: their order is of no matter).
 //
-//   KS = 8: the eight waves of a workgroup share 16 channels, each taking every
-//           eighth 128 bytes of K, and add their sums in LDS: short products,
-//           where the time is one round trip to memory.
-//   KS = 1: a wave takes 16 channels over all of K, with no barrier: many
-//           channels (the LM head).
+// The workgroups running at one time read neighbouring rows (turn i goes to
+// workgroup i % grid). At 262144 channels of K = 2816 one token takes 126 us,
+// 5.9 TB/s of weights, five from fp32 134 us; giving each workgroup one
+// contiguous run of channels took 133 us, more loads in flight (8 or 12
+// fragments a wave) or copies into LDS in whole lines changed nothing, and
+// non-temporal loads cost 12 us.
 #include "int8_common.hpp"
 #include "int8_quant.hpp"
 
@@ -26,18 +29,67 @@ constexpr int kHeld = 3;                 // units in flight per wave
 __host__ __device__ constexpr int code_stride(int K) { return (K + kUnit - 1) / kUnit * kUnit + 16; }
 
 // The tokens' codes into LDS, zero from K to the end of its last unit, and the
-// scales: quantised from activations of type Tx, a wave per row.
+// scales: quantised from activations of type Tx by the whole workgroup, eight
+// values a thread at a time. The codes' rows are whole 128 bytes, so sixteen
+// neighbouring threads always share a row; the first kKeep vectors of a thread
+// stay in registers between the rows' maxima and the codes.
 template <class Tx>
-__device__ inline void codes_from(const I8FewArgs &a, char *codes, float *s_xs)
+__device__ inline void codes_from(const I8FewArgs &a, char *codes, float *s_xs, uint32_t *s_top, RowScale *s_rs)
 {
-    const int lane = threadIdx.x & 63;
-    const int stride = code_stride(a.g.K);
-    for (int t = threadIdx.x >> 6; t < a.g.T; t += kI8Waves) {
-        const Tx *row = reinterpret_cast<const Tx *>(a.x) + (size_t)t * a.ld;
-        const float sc = quantize_row<Tx>(row, a.k_x, stride - 16, codes + t * stride, lane);
-        if (lane == 0)
-            s_xs[t] = sc;
+    constexpr int kKeep = 4;
+    const int stride = code_stride(a.g.K), pieces = (stride - 16) / 8;
+    const int total = a.g.T * pieces;
+    if ((int)threadIdx.x < a.g.T)
+        s_top[threadIdx.x] = 0u;
+    __syncthreads();
+    typename Vec8<Tx>::type v[kKeep];
+    // i / pieces, exact for i * pieces < 2^32: i < total <= 15360 here
+    auto row_of = [&](int i) { return (int)__umulhi((uint32_t)i, a.row_magic); };
+    auto load = [&](int i) {
+        const int t = row_of(i), k = (i - t * pieces) * 8;
+        return load8<Tx>(reinterpret_cast<const Tx *>(a.x) + (size_t)t * a.ld, k, a.k_x);
+    };
+    auto rank = [&](typename Vec8<Tx>::type q, int i) {
+        uint32_t top = top8(q);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            top = max(top, (uint32_t)__shfl_xor((int)top, o));
+        if ((threadIdx.x & 15) == 0)
+            atomicMax(&s_top[row_of(i)], top);
+    };
+    // total is a multiple of 16: a group of 16 threads is in or out together
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = (int)threadIdx.x + j * kI8Threads;
+        if (i < total)
+            v[j] = load(i);
     }
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = (int)threadIdx.x + j * kI8Threads;
+        if (i < total)
+            rank(v[j], i);
+    }
+    for (int i = (int)threadIdx.x + kKeep * kI8Threads; i < total; i += kI8Threads)
+        rank(load(i), i);
+    __syncthreads();
+    if ((int)threadIdx.x < a.g.T) {
+        s_rs[threadIdx.x] = row_scales(s_top[threadIdx.x]);
+        s_xs[threadIdx.x] = s_rs[threadIdx.x].s;
+    }
+    __syncthreads();
+    auto emit = [&](typename Vec8<Tx>::type q, int i) {
+        const int t = row_of(i), k = (i - t * pieces) * 8;
+        *reinterpret_cast<uint2 *>(codes + t * stride + k) = codes8<Tx>(q, s_rs[t]);
+    };
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = (int)threadIdx.x + j * kI8Threads;
+        if (i < total)
+            emit(v[j], i);
+    }
+    for (int i = (int)threadIdx.x + kKeep * kI8Threads; i < total; i += kI8Threads)
+        emit(load(i), i);
 }
 
 __device__ inline void codes_copied(const I8FewArgs &a, char *codes, float *s_xs)
@@ -54,39 +106,36 @@ __device__ inline void codes_copied(const I8FewArgs &a, char *codes, float *s_xs
         s_xs[threadIdx.x] = a.g.xs[threadIdx.x];
 }
 
-template <int TB, int KS, class Ty>
+template <int TB, class Ty>
 __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
 {
     __shared__ float s_xs[16 * TB];
-    __shared__ i32x4 s_red[KS == 1 ? 1 : 2][KS == 1 ? 1 : kI8Waves][TB][64];
-    extern __shared__ char s_codes[];    // [T][code_stride(K)]
+    __shared__ uint32_t s_top[16 * TB];
+    __shared__ RowScale s_rs[16 * TB];
+    __shared__ i32x4 s_red[2][kI8Waves][TB][64];
+    extern __shared__ __attribute__((aligned(16))) char s_codes[];    // [T][code_stride(K)]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r = lane & 15, p = lane >> 4;
     const int stride = code_stride(a.g.K);
     const int units = (a.g.K + kUnit - 1) / kUnit;
-    // this wave's items (16 channels each): a contiguous run
-    const int items = (a.g.N + 15) / 16;
-    const int takers = KS == 1 ? (int)gridDim.x * kI8Waves : (int)gridDim.x;
-    const int me = KS == 1 ? (int)blockIdx.x * kI8Waves + wave : (int)blockIdx.x;
-    const int per = items / takers, rest = items % takers;
-    int it = me * per + min(me, rest);
-    const int end = it + per + (me < rest ? 1 : 0);
-    const int first = KS == 1 ? 0 : wave;                  // the wave's units: first, first + KS, ...
-    const int mine = (units - first + KS - 1) / KS;        // (it may have none)
-    const int batches = max(1, (units + KS * kHeld - 1) / (KS * kHeld));
+    const int items = (a.g.N + 15) / 16;                   // of 16 channels
+    const int mine = (units - wave + kI8Waves - 1) / kI8Waves;    // this wave's units: wave, wave + 8, ... (maybe none)
+    const int batches = (units + kI8Waves * kHeld - 1) / (kI8Waves * kHeld);
+    int it = (int)blockIdx.x * a.run;
 
     struct Source {
         rsrc_t rsrc;
         uint32_t lane;
         int u;
     };
+    // one step's weights (past the last item: none, zeros are read)
     auto source = [&](int item, int b) {
         const int i = min(item, items - 1);
         const int rows = min(16, a.g.N - i * 16);
         Source q;
         q.rsrc = make_rsrc(a.g.wq + (size_t)i * 16 * a.g.ldw,
-                           item < end ? (uint32_t)(rows - 1) * (uint32_t)a.g.ldw + (uint32_t)a.g.K : 0u);
+                           item < items ? (uint32_t)(rows - 1) * (uint32_t)a.g.ldw + (uint32_t)a.g.K : 0u);
         q.lane = (uint32_t)min(r, rows - 1) * (uint32_t)a.g.ldw + (uint32_t)(p * 16);
         q.u = b * kHeld;
         return q;
@@ -95,7 +144,7 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
     // codes (or zero), which meet zeros of x
     auto load_weight = [&](const Source &q, int j, int h) {
         const int u = q.u + j;
-        const uint32_t at = (uint32_t)((first + u * KS) * kUnit + h * 64);
+        const uint32_t at = (uint32_t)((wave + u * kI8Waves) * kUnit + h * 64);
         return __builtin_bit_cast(i32x4, load16(q.rsrc, u < mine ? q.lane + at : 0x80000000u, 0));
     };
 
@@ -109,23 +158,25 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
                 w[j][h] = load_weight(q, j, h);
     }
     switch (a.x_type) {
-    case DGW4_F32: codes_from<float>(a, s_codes, s_xs); break;
-    case DGW4_F16: codes_from<_Float16>(a, s_codes, s_xs); break;
-    case DGW4_BF16: codes_from<__bf16>(a, s_codes, s_xs); break;
+    case DGW4_F32: codes_from<float>(a, s_codes, s_xs, s_top, s_rs); break;
+    case DGW4_F16: codes_from<_Float16>(a, s_codes, s_xs, s_top, s_rs); break;
+    case DGW4_BF16: codes_from<__bf16>(a, s_codes, s_xs, s_top, s_rs); break;
     default: codes_copied(a, s_codes, s_xs);
     }
     __syncthreads();
-    const bool vec = rows_in_fours<Ty>(a.g);
     const char *xp[TB];
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb)
         xp[tb] = s_codes + min(tb * 16 + r, a.g.T - 1) * stride + p * 16;
     int buf = 0;
     i32x4 acc[TB];
-    for (int b = 0; it < end;) {
+    for (int b = 0; it < items;) {
         const bool last = b == batches - 1;
-        const int nit = last ? it + 1 : it, nb = last ? 0 : b + 1;
+        const int nit = !last ? it : (it + 1) % a.run ? it + 1 : it + 1 + ((int)gridDim.x - 1) * a.run, nb = last ? 0 : b + 1;
         const Source q = source(nit, nb);
+        // the scale of the channel this thread stores, ahead of the next weights
+        float ws = a.g.ws[min(it * 16 + (int)(threadIdx.x & 15), a.g.N - 1)];
+        asm volatile("" : : : "memory");
         if (b == 0) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
@@ -134,7 +185,7 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
             // past the wave's last unit the weights are zero
-            const int at = min(first + (b * kHeld + j) * KS, units - 1) * kUnit;
+            const int at = min(wave + (b * kHeld + j) * kI8Waves, units - 1) * kUnit;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -144,62 +195,51 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
                 w[j][h] = load_weight(q, j, h);    // the next step's, into the registers just read
             }
         }
+        asm volatile("" : "+v"(ws));     // waited for here, where the count of loads after it is known
         if (last) {
-            const int n0 = it * 16;
-            if constexpr (KS == 1) {
-                const f32x4 ws = channel_scales(a.g, n0 + 4 * p);
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb) {
-                    const int t = tb * 16 + r;
-                    if (t < a.g.T)
-                        store4<Ty>((Ty *)a.g.y + (size_t)t * a.g.ldy, n0 + 4 * p, a.g.N, vec, acc[tb], s_xs[t], ws);
-                }
-            } else {
+            for (int tb = 0; tb < TB; ++tb)
+                s_red[buf][wave][tb][lane] = acc[tb];
+            __syncthreads();
+            // one output per thread: token i, channel c
+            const int c = threadIdx.x & 15, n = it * 16 + c;
+            for (int i = threadIdx.x >> 4; i < a.g.T && n < a.g.N; i += kI8Threads / 16) {
+                int sum = 0;
 #pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-                    s_red[buf][wave][tb][lane] = acc[tb];
-                __syncthreads();
-                // one output per thread: token i, channel c
-                for (int o = threadIdx.x; o < a.g.T * 16; o += kI8Threads) {
-                    const int i = o >> 4, c = o & 15;
-                    if (n0 + c < a.g.N) {
-                        int sum = 0;
-#pragma unroll
-                        for (int v = 0; v < kI8Waves; ++v)
-                            sum += s_red[buf][v][i >> 4][(c >> 2) * 16 + (i & 15)][c & 3];
-                        ((Ty *)a.g.y)[(size_t)i * a.g.ldy + n0 + c] = scaled<Ty>(sum, s_xs[i], a.g.ws[n0 + c]);
-                    }
-                }
-                buf ^= 1;
+                for (int v = 0; v < kI8Waves; ++v)
+                    sum += s_red[buf][v][i >> 4][(c >> 2) * 16 + (i & 15)][c & 3];
+                ((Ty *)a.g.y)[(size_t)i * a.g.ldy + n] = scaled<Ty>(sum, s_xs[i], ws);
             }
+            buf ^= 1;                    // two barriers lie between a buffer's reads and its next writes
         }
         it = nit;
         b = nb;
     }
 }
 
-template <int TB, int KS, class Ty>
-hipError_t run(const I8FewArgs &a, hipStream_t st)
+template <int TB, class Ty>
+hipError_t run(I8FewArgs a, hipStream_t st)
 {
     static size_t allowed = 24 * 1024;
     const size_t lds = (size_t)a.g.T * code_stride(a.g.K);
-    const hipError_t err = allow_lds(i8_few_kernel<TB, KS, Ty>, lds, allowed);
+    const hipError_t err = allow_lds(i8_few_kernel<TB, Ty>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int items = (a.g.N + 15) / 16;
-    const int groups = KS == 1 ? (items + kI8Waves - 1) / kI8Waves : items;
-    const int most = lds <= 24 * 1024 ? 1024 : lds <= 56 * 1024 ? 512 : 256;     // resident at once
-    i8_few_kernel<TB, KS, Ty><<<dim3(groups < most ? groups : most), dim3(kI8Threads), lds, st>>>(a);
+    const int most = lds <= 60 * 1024 ? 512 : 256;         // resident at once
+    // with many turns to share out, two neighbouring blocks a turn: a row's
+    // stores then fill whole cache lines in one L2 (16 tokens, 262144 channels
+    // of fp32: 149 -> 144 us; at 65536 channels the coarser turns cost 1 us)
+    a.run = items >= 16 * most ? 2 : 1;
+    const int turns = (items + a.run - 1) / a.run;
+    i8_few_kernel<TB, Ty><<<dim3(turns < most ? turns : most), dim3(kI8Threads), lds, st>>>(a);
     return hipGetLastError();
 }
 
 template <class Ty>
 hipError_t pick(const I8FewArgs &a, hipStream_t st)
 {
-    const bool wide = a.g.N >= kI8FewWideN;
-    if (a.g.T <= 16)
-        return wide ? run<1, 1, Ty>(a, st) : run<1, 8, Ty>(a, st);
-    return wide ? run<2, 1, Ty>(a, st) : run<2, 8, Ty>(a, st);
+    return a.g.T <= 16 ? run<1, Ty>(a, st) : run<2, Ty>(a, st);
 }
 
 }  // namespace
@@ -209,8 +249,10 @@ bool i8_few_fits(int T, int K)
     return T <= kI8FewTokens && (size_t)T * code_stride(K) <= 120 * 1024;
 }
 
-hipError_t launch_i8_few(const I8FewArgs &a, hipStream_t stream)
+hipError_t launch_i8_few(I8FewArgs a, hipStream_t stream)
 {
+    const uint32_t pieces = (uint32_t)(code_stride(a.g.K) - 16) / 8;
+    a.row_magic = (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
     return a.g.type == DGW4_F32   ? pick<float>(a, stream)
            : a.g.type == DGW4_F16 ? pick<_Float16>(a, stream)
                                   : pick<__bf16>(a, stream);

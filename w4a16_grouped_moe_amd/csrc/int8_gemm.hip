@@ -17,31 +17,11 @@
 #include "int8_common.hpp"
 
 #include <cmath>
-#include <stdlib.h>
 
 namespace dgw4 {
 namespace {
 
 constexpr int kStageK = 128;                     // bytes of K per stage
-constexpr uint32_t kPast = 0x80000000u;          // an offset past every buffer here
-
-// 64 lanes x 16 bytes from the buffer into LDS at lds (wave-uniform), lane
-// after lane. No register receives the data; the caller waits on vmcnt.
-__device__ inline void copy_to_lds(rsrc_t r, uint32_t voff, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(r)
-                 : "memory");
-}
-
-// All of this wave's LDS reads have returned and at most N of its copies are
-// still in flight; then the workgroup's barrier.
-template <int N>
-__device__ inline void stage_barrier()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
-}
 
 template <int BN, int BT, int WN, int WT, int ST, class Ty>
 __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8Args a, int tiles_n, int tiles_t)
@@ -187,8 +167,6 @@ hipError_t pick(const I8Args &a, hipStream_t st)
     for (int i = 1; i < 5; ++i)
         if (est[i] < est[best])
             best = i;
-    const char *e = getenv("DGW4_FORCE");
-    if (e) best = atoi(e);
     switch (best) {
     case 0: return run<256, 256, 64, 128, 2, Ty>(a, st);
     case 1: return run<256, 128, 64, 64, 3, Ty>(a, st);

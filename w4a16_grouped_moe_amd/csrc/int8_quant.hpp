@@ -38,15 +38,39 @@ __device__ inline typename Vec8<Tx>::type load8(const Tx *row, int k, int K)
     return v;
 }
 
-// The bits of the largest magnitude; above those of infinity if there is a NaN.
-template <class Tx>
-__device__ inline uint32_t top8(typename Vec8<Tx>::type v, uint32_t top)
+// The largest magnitude among eight values as fp32 bits; above those of
+// infinity if there is a NaN. The 16-bit types are ranked as they are, two at
+// a time: without the sign, a float's bits are in the floats' order.
+__device__ inline uint32_t top8(Vec8<float>::type v)
 {
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        top = max(top, __builtin_bit_cast(uint32_t, to_f32((Tx)v[i])) & 0x7FFFFFFFu);
+        top = max(top, __builtin_bit_cast(uint32_t, (float)v[i]) & 0x7FFFFFFFu);
     return top;
 }
+
+template <class V>
+__device__ inline uint32_t top8_16(V v)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const uint4 u = __builtin_bit_cast(uint4, v);
+    const uint32_t m = 0x7FFF7FFFu;
+    auto mx = [](uint32_t x, uint32_t y) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, x),
+                                                                      __builtin_bit_cast(u16x2, y)));
+    };
+    const uint32_t t = mx(mx(u.x & m, u.y & m), mx(u.z & m, u.w & m));
+    return max(t & 0xFFFFu, t >> 16);
+}
+
+__device__ inline uint32_t top8(Vec8<_Float16>::type v)
+{
+    const uint32_t t = top8_16(v);
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)t)) & 0x7FFFFFFFu;
+}
+
+__device__ inline uint32_t top8(Vec8<__bf16>::type v) { return top8_16(v) << 16; }
 
 __device__ inline float row_scale(uint32_t top)
 {
@@ -56,33 +80,49 @@ __device__ inline float row_scale(uint32_t top)
     return s == 0.0f ? 1.0f : s;
 }
 
-// Whether a row of this scale may take the reciprocal: 1 / s and x / s within
-// fp32's normal range.
-__device__ inline bool reciprocal_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
+// What a row's codes are made with: its scale, the scale's reciprocal (0 where
+// every vector divides: 1 / s or x / s could leave fp32's normal range) and
+// whether the row is finite.
+struct RowScale {
+    float s, inv;
+    bool finite;
+};
+
+__device__ inline RowScale row_scales(uint32_t top)
+{
+    RowScale r;
+    r.s = row_scale(top);
+    r.finite = top < 0x7F800000u;
+    r.inv = r.s >= 1e-30f && r.s <= 1e30f ? __fdiv_rn(1.0f, r.s) : 0.0f;
+    return r;
+}
 
 template <class Tx>
-__device__ inline uint2 codes8(typename Vec8<Tx>::type v, float s, float inv, bool fast, bool finite)
+__device__ inline uint2 codes8(typename Vec8<Tx>::type v, const RowScale &rs)
 {
     float q[8], off = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = __fmul_rn(to_f32((Tx)v[i]), inv);
+        const float t = __fmul_rn(to_f32((Tx)v[i]), rs.inv);
         q[i] = rintf(t);
         off = fmaxf(off, fabsf(__fsub_rn(t, q[i])));
     }
-    if (!fast || off > kNearHalf) {
+    if (rs.inv == 0.0f || off > kNearHalf) {
+        // here alone a quotient can pass 127: where the scale is subnormal
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            q[i] = rintf(__fdiv_rn(to_f32((Tx)v[i]), s));
+            q[i] = fminf(fmaxf(rintf(__fdiv_rn(to_f32((Tx)v[i]), rs.s)), -127.0f), 127.0f);
     }
     uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        b[i] = (uint32_t)(int)fminf(fmaxf(q[i], -127.0f), 127.0f) & 0xFFu;
+        b[i] = (uint32_t)(int)q[i];
+    // the low bytes of two, then of four words
+    auto pair = [](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x0C0C0400u); };
     uint2 o;
-    o.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-    o.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
-    return finite ? o : make_uint2(0, 0);
+    o.x = pair(b[0], b[1]) | pair(b[2], b[3]) << 16;
+    o.y = pair(b[4], b[5]) | pair(b[6], b[7]) << 16;
+    return rs.finite ? o : make_uint2(0, 0);
 }
 
 __device__ inline uint32_t wave_top(uint32_t v)
@@ -93,36 +133,43 @@ __device__ inline uint32_t wave_top(uint32_t v)
     return v;
 }
 
-// A row by one wave into q[0 .. end) (8-byte aligned, end a multiple of 16,
-// zero from K on); returns the scale, in every lane. Rows of up to 64 * 8 *
-// kKept values are read once.
-template <class Tx>
-__device__ inline float quantize_row(const Tx *__restrict__ row, int K, int end, char *q, int lane)
+// Vector i (eight values) of a row by threads tid of N (a wave, or a workgroup
+// with room for its waves' maxima in s_part): the row's codes into q[0 .. end)
+// (8-byte aligned, end a multiple of 16, zero from K on); returns the scale in
+// every thread. The first kKept vectors of a thread stay in registers between
+// the maximum and the codes.
+template <class Tx, int N, int kKept>
+__device__ inline float quantize_row(const Tx *__restrict__ row, int K, int end, char *q, int tid, uint32_t *s_part)
 {
-    constexpr int kKept = 6;
     typename Vec8<Tx>::type v[kKept];
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < kKept; ++j)
-        v[j] = load8<Tx>(row, (j * 64 + lane) * 8, K);
+        v[j] = load8<Tx>(row, (j * N + tid) * 8, K);
 #pragma unroll
     for (int j = 0; j < kKept; ++j)
-        top = top8<Tx>(v[j], top);
-    for (int k = (kKept * 64 + lane) * 8; k < K; k += 512)
-        top = top8<Tx>(load8<Tx>(row, k, K), top);
+        top = max(top, top8(v[j]));
+    for (int k = (kKept * N + tid) * 8; k < K; k += N * 8)
+        top = max(top, top8(load8<Tx>(row, k, K)));
     top = wave_top(top);
-    const float s = row_scale(top);
-    const bool finite = top < 0x7F800000u, fast = reciprocal_ok(s);
-    const float inv = __fdiv_rn(1.0f, s);
+    if constexpr (N > 64) {
+        if ((tid & 63) == 0)
+            s_part[tid >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N / 64; ++i)
+            top = max(top, s_part[i]);
+    }
+    const RowScale rs = row_scales(top);
 #pragma unroll
     for (int j = 0; j < kKept; ++j) {
-        const int k = (j * 64 + lane) * 8;
+        const int k = (j * N + tid) * 8;
         if (k < end)
-            *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(v[j], s, inv, fast, finite);
+            *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(v[j], rs);
     }
-    for (int k = (kKept * 64 + lane) * 8; k < end; k += 512)
-        *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(load8<Tx>(row, k, K), s, inv, fast, finite);
-    return s;
+    for (int k = (kKept * N + tid) * 8; k < end; k += N * 8)
+        *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(load8<Tx>(row, k, K), rs);
+    return rs.s;
 }
 
 }  // namespace
