@@ -8,7 +8,6 @@ an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -517,58 +516,86 @@ def moe_few_workspace_bytes(T: int, topk: int, E: int, d: int, m: int, gu_g: int
     return int(n.value)
 
 
-def _same_device(t: torch.Tensor, **others) -> None:
-    for name, o in others.items():
-        if o.device != t.device:
-            raise ValueError(f"{name} is on {o.device}, not {t.device}")
+# The entry points below run a few microseconds of GPU work per call, so their
+# host side is kept short: one integer per tensor for its device, the raw
+# stream handle, no context manager where the device is the current one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(t: torch.Tensor):
-    """The tensor's device as the current one while a call is enqueued."""
-    if torch.cuda.current_device() == t.device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+def _gpu(t, name: str) -> int:
+    """The index of a tensor's ROCm device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be on a ROCm device, got {t.device}")
+    return d
+
+
+def _flat(t, name: str, dtypes, d: int) -> int:
+    """Pointer of a contiguous tensor on device d."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != d:
+        raise ValueError(f"{name} is on {t.device}, not on the ROCm device cuda:{d}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn: str, d: int, *args) -> None:
+    """Enqueue one call on device d's current stream, with that device the
+    current one for the call."""
+    f = getattr(_lib or lib(), fn)
+    st = _raw_stream(d) if _raw_stream else torch.cuda.current_stream(d).cuda_stream
+    if torch.cuda.current_device() == d:
+        status = f(*args, st)
+    else:
+        with torch.cuda.device(d):
+            status = f(*args, st)
+    if status != OK:
+        raise Dgw4Error(fn, status)
+
+
+_U8, _I32, _F32, _I8 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.int8,)
 
 
 def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, out) -> torch.Tensor:
     """The arguments that moe_few and moe_few_routed share; route = their
-    routing tensors (checked by the caller)."""
+    routing tensors, (tensor, name, dtypes) each (shapes checked by the
+    caller)."""
     gq, gs, gz, gg = gu
     dq, ds, dz, dg = dn
+    d_ = _gpu(x, "x")
     if x.dim() != 2 or gq.dim() != 3 or dq.dim() != 3:
         raise ValueError("x must be [T, d], the packed stacks [E, N, K/2]")
     T, d = x.shape
-    E = gq.shape[0]
-    m = dq.shape[2] * 2
-    if gq.shape != (E, 2 * m, d // 2) or dq.shape != (E, d, m // 2):
+    E, m2, _ = gshape = gq.shape
+    m = m2 // 2
+    if gshape != (E, 2 * m, d // 2) or dq.shape != (E, d, m // 2):
         raise ValueError(f"packed shapes {tuple(gq.shape)} / {tuple(dq.shape)} do not match "
                          f"x {tuple(x.shape)}")
     if _group(gg) < 1 or _group(dg) < 1:
         raise ValueError("group sizes must be positive")
-    if gs.shape != (E, 2 * m, d // _group(gg)) or gz.shape != gs.shape:
+    if gs.shape != (E, m2, d // _group(gg)) or gz.shape != gs.shape:
         raise ValueError("gate_up scale/zero shape mismatch")
     if ds.shape != (E, d, m // _group(dg)) or dz.shape != ds.shape:
         raise ValueError("down scale/zero shape mismatch")
-    ptrs = [_dev(x, "x", _F16), *(_dev(t, n, ty) for t, n, ty in route),
-            _dev(gq, "gu_q", (torch.uint8,)), _dev(gs, "gu_s", _F16), _dev(gz, "gu_z", _F16),
-            _dev(dq, "dn_q", (torch.uint8,)), _dev(ds, "dn_s", _F16), _dev(dz, "dn_z", _F16)]
     if workspace is None:
         need = moe_few_workspace_bytes(T, topk, E, d, m, gg, dg)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
-    pws = _dev(workspace, "workspace", (torch.uint8,))
     if out is None:
         out = torch.empty((T, d), dtype=torch.float16, device=x.device)
-    if out.shape != (T, d):
+    elif out.shape != (T, d):
         raise ValueError("out must be [T, d]")
-    pout = _dev(out, "out", _F16)
-    _same_device(x, gu_q=gq, gu_s=gs, gu_z=gz, dn_q=dq, dn_s=ds, dn_z=dz, workspace=workspace,
-                 out=out, **{n: t for t, n, _ in route})
-    n = ctypes.c_size_t(workspace.numel())
-    i = 1 + len(route)
-    with _on(x):
-        _check(fn, getattr(lib(), fn)(
-            *ptrs[:i], T, topk, E, d, m, ptrs[i], ptrs[i + 1], ptrs[i + 2], gg, ptrs[i + 3],
-            ptrs[i + 4], ptrs[i + 5], dg, pws, ctypes.byref(n), pout, _stream(x)))
+    _call(fn, d_, _flat(x, "x", _F16, d_), *[_flat(t, n, ty, d_) for t, n, ty in route],
+          T, topk, E, d, m,
+          _flat(gq, "gu_q", _U8, d_), _flat(gs, "gu_s", _F16, d_), _flat(gz, "gu_z", _F16, d_), gg,
+          _flat(dq, "dn_q", _U8, d_), _flat(ds, "dn_s", _F16, d_), _flat(dz, "dn_z", _F16, d_), dg,
+          _flat(workspace, "workspace", _U8, d_), ctypes.byref(ctypes.c_size_t(workspace.numel())),
+          _flat(out, "out", _F16, d_))
     return out
 
 
@@ -601,20 +628,22 @@ def moe_few_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, gu: 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-def _rows(t: torch.Tensor, name: str, dtypes) -> tuple[int, int]:
-    """Pointer and row distance of a 2-d device tensor whose rows are
+def _rows(t: torch.Tensor, name: str, dtypes, d: int) -> tuple[int, int]:
+    """Pointer and row distance of a 2-d tensor on device d whose rows are
     contiguous but may lie apart (a slice of a wider tensor)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a ROCm device, got {t.device}")
+    if t.get_device() != d:
+        raise ValueError(f"{name} is on {t.device}, not on the ROCm device cuda:{d}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (cols > 1 and step != 1) or ld < cols:
         raise ValueError(f"{name}: the elements of a row must be contiguous, its rows must not overlap")
     return t.data_ptr(), ld
 
@@ -627,20 +656,19 @@ def quantize_rows_i8(x: torch.Tensor, out: tuple | None = None):
     """Symmetric 8-bit quantisation of each row of x (fp32, fp16 or bf16
     [rows, K]; rows may lie apart): (q int8 [rows, K rounded up to 16], the
     added columns zero, s fp32 [rows]). ``out`` = (q, s) to write into."""
-    px, ldx = _rows(x, "x", _TYPES)
+    d = _gpu(x, "x")
+    px, ldx = _rows(x, "x", _TYPES, d)
     rows, K = x.shape
+    Kp = _up16(K)
     if out is None:
-        out = (torch.empty((rows, _up16(K)), dtype=torch.int8, device=x.device),
+        out = (torch.empty((rows, Kp), dtype=torch.int8, device=x.device),
                torch.empty(rows, dtype=torch.float32, device=x.device))
     q, s = out
-    pq, ldq = _rows(q, "q", (torch.int8,))
-    ps = _dev(s, "s", (torch.float32,))
-    if q.shape != (rows, _up16(K)) or s.shape != (rows,):
+    if q.shape != (rows, Kp) or s.shape != (rows,):
         raise ValueError("out must be (q [rows, K rounded up to 16], s [rows])")
-    _same_device(x, q=q, s=s)
-    with _on(x):
-        _check("dgw4_quantize_rows_i8", lib().dgw4_quantize_rows_i8(
-            px, _TYPES[x.dtype], rows, K, ldx, pq, ldq, ps, _stream(x)))
+    pq, ldq = _rows(q, "q", _I8, d)
+    _call("dgw4_quantize_rows_i8", d, px, _TYPES[x.dtype], rows, K, ldx, pq, ldq,
+          _flat(s, "s", _F32, d))
     return q, s
 
 
@@ -648,10 +676,10 @@ def _w8a8_out(x, N: int, dtype, out):
     if out is None:
         if dtype not in _TYPES:
             raise TypeError(f"dtype {dtype} not in {tuple(_TYPES)}")
-        out = torch.empty((x.shape[0], N), dtype=dtype, device=x.device)
-    elif out.shape != (x.shape[0], N):
+        return torch.empty((x.shape[0], N), dtype=dtype, device=x.device)
+    if out.shape != (x.shape[0], N):
         raise ValueError("out must be [T, N]")
-    return out, *_rows(out, "out", _TYPES)
+    return out
 
 
 def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
@@ -663,19 +691,18 @@ def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor 
     ``dtype`` (fp16, bf16, fp32), or written into ``out``, whose type counts
     then. See dgw4_w8a8_linear in include/dgw4.h."""
     wq, ws = w
-    px, ldx = _rows(xq, "xq", (torch.int8,))
-    pw, ldw = _rows(wq, "wq", (torch.int8,))
-    pxs, pws = _dev(xs, "xs", (torch.float32,)), _dev(ws, "ws", (torch.float32,))
+    d = _gpu(xq, "xq")
+    px, ldx = _rows(xq, "xq", _I8, d)
+    pw, ldw = _rows(wq, "wq", _I8, d)
     T, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K or xs.shape != (T,) or ws.shape != (N,):
+    N, Kw = wq.shape
+    if Kw != K or xs.shape != (T,) or ws.shape != (N,):
         raise ValueError(f"wq {tuple(wq.shape)}, xs {tuple(xs.shape)}, ws {tuple(ws.shape)} do not "
                          f"match xq {tuple(xq.shape)}")
-    out, py, ldy = _w8a8_out(xq, N, dtype, out)
-    _same_device(xq, xs=xs, wq=wq, ws=ws, out=out)
-    with _on(xq):
-        _check("dgw4_w8a8_linear", lib().dgw4_w8a8_linear(
-            px, pxs, T, K, ldx, pw, pws, N, ldw, py, _TYPES[out.dtype], ldy, _stream(xq)))
+    out = _w8a8_out(xq, N, dtype, out)
+    py, ldy = _rows(out, "out", _TYPES, d)
+    _call("dgw4_w8a8_linear", d, px, _flat(xs, "xs", _F32, d), T, K, ldx, pw,
+          _flat(ws, "ws", _F32, d), N, ldw, py, _TYPES[out.dtype], ldy)
     return out
 
 
@@ -696,21 +723,18 @@ def w8a8_linear_tokens(x: torch.Tensor, w: tuple, out: torch.Tensor | None = Non
     ``workspace``: uint8 of at least w8a8_workspace_bytes(T, K), allocated here
     when not given."""
     wq, ws = w
-    px, ldx = _rows(x, "x", _TYPES)
-    pw, ldw = _rows(wq, "wq", (torch.int8,))
-    pws = _dev(ws, "ws", (torch.float32,))
+    d = _gpu(x, "x")
+    px, ldx = _rows(x, "x", _TYPES, d)
+    pw, ldw = _rows(wq, "wq", _I8, d)
     T, K = x.shape
-    N = wq.shape[0]
-    if wq.shape[1] != _up16(K) or ws.shape != (N,):
+    N, Kw = wq.shape
+    if Kw != _up16(K) or ws.shape != (N,):
         raise ValueError(f"wq {tuple(wq.shape)}, ws {tuple(ws.shape)} do not match x {tuple(x.shape)}")
-    out, py, ldy = _w8a8_out(x, N, dtype, out)
+    out = _w8a8_out(x, N, dtype, out)
+    py, ldy = _rows(out, "out", _TYPES, d)
     if workspace is None:
         workspace = torch.empty(max(w8a8_workspace_bytes(T, K), 1), dtype=torch.uint8, device=x.device)
-    pb = _dev(workspace, "workspace", (torch.uint8,))
-    _same_device(x, wq=wq, ws=ws, out=out, workspace=workspace)
-    n = ctypes.c_size_t(workspace.numel())
-    with _on(x):
-        _check("dgw4_w8a8_linear_tokens", lib().dgw4_w8a8_linear_tokens(
-            px, _TYPES[x.dtype], T, K, ldx, pw, pws, N, ldw, py, _TYPES[out.dtype], ldy, pb,
-            ctypes.byref(n), _stream(x)))
+    _call("dgw4_w8a8_linear_tokens", d, px, _TYPES[x.dtype], T, K, ldx, pw,
+          _flat(ws, "ws", _F32, d), N, ldw, py, _TYPES[out.dtype], ldy,
+          _flat(workspace, "workspace", _U8, d), ctypes.byref(ctypes.c_size_t(workspace.numel())))
     return out
