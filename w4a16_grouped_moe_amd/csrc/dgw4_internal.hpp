@@ -156,8 +156,14 @@ struct FewArgs {
     const uint16_t *dn_s, *dn_z;
     int gu_tiled, dn_tiled;
     uint16_t *h;                // fp16 [A, m], columns permuted per 8 (workspace)
+    float *y;                   // fp32 [A, d], each assignment's output (workspace); null: kept in LDS
     uint16_t *out;              // fp16 [T, d]
 };
+
+// Up to this many assignments down weights and sums the experts' outputs
+// itself; with more, a third launch does (see moe_few.hip).
+constexpr int kFewSumInside = 16;
+bool few_keeps_outputs(int A);
 
 // The groups of d and of m the two kernels keep scales for.
 constexpr int kFewMaxUpGroups = 64, kFewMaxDownGroups = 32;

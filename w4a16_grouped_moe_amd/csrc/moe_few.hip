@@ -6,9 +6,8 @@
 //            16) assignments of one tile and splits d over its eight waves.
 //   down     out[t, c] = sum_k w[t, k] (H[a] Wd_e^T)[c], k ascending; a
 //            workgroup takes 16 output columns for every assignment, a wave
-//            one half of m for one tile at a time, and keeps the experts'
-//            outputs in LDS in fp32 until they are weighted and summed in k
-//            order.
+//            one tile at a time, and keeps the experts' outputs in LDS in
+//            fp32 until they are weighted and summed in k order.
 //
 // The layer is bound by the experts' weights, read once each, so both
 // launches split the weights over the whole chip (44 column blocks per expert
@@ -30,15 +29,21 @@
 namespace dgw4 {
 namespace {
 
+#ifndef DGRID
+#define DGRID 512
+#endif
 constexpr int kUpThreads = 512, kUpWaves = kUpThreads / 64;
 constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / 64;
 constexpr int kSmallAssign = 64;         // assignments that one wave sorts
 constexpr int kFewRouteExperts = 256;    // experts that one wave routes over in registers
+constexpr uint32_t kFewPast = 0x80000000u;   // an offset past every buffer here, small additions included
 
 // Columns of K that one lane-load of packed weights covers are a group G; a
 // wave holds this many groups of weights and activations at once.
 template <int G>
 constexpr int kBatch = G == 128 ? 3 : 6;
+template <int G>
+constexpr int kItemBatch = G == 128 ? 6 : 11;    // in few_down_items_kernel
 
 // The tile list of one workgroup: tile i holds the assignments row[start ..
 // start + n) (low half, their tokens in the high half).
@@ -52,8 +57,20 @@ struct FewTiles {
 };
 static_assert(16 * kSmallAssign >= kFewMaxAssign, "the row list holds either form");
 
+// Keeps the loads before it ahead of those after it (everything else may
+// cross): loads return in order, and a wait counts the ones issued since, so
+// the order in which a step's loads go out has to be the order of their use.
+__device__ inline void keep_load_order() { __builtin_amdgcn_sched_barrier(0x38F); }
+
 // A value that every lane of the wave holds, as a scalar.
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <class P>
+__device__ inline const P *uniform(const P *p)
+{
+    const uint64_t v = (uint64_t)p;
+    return (const P *)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
 
 __device__ inline uint32_t tile_at(const FewTiles &s, int i) { return (uint32_t)uniform((int)s.tile[i]); }
 __device__ inline int tile_expert_of(uint32_t t) { return (int)(t & 0x3FF); }
@@ -272,60 +289,65 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     }
     const int items = uniform(s.tiles) * cblocks;
     const int per = items / gridDim.x, rest = items % gridDim.x;
-    int it = (int)blockIdx.x * per + min((int)blockIdx.x, rest);
-    const int end = it + per + ((int)blockIdx.x < rest ? 1 : 0);
-    if (it >= end)
+    const int first = uniform((int)blockIdx.x * per + min((int)blockIdx.x, rest));
+    const int count = uniform(per + ((int)blockIdx.x < rest ? 1 : 0));
+    if (count == 0)
         return;                          // the whole workgroup: no barrier below is missed
     const int batches = (groups + kUpWaves * NB - 1) / (kUpWaves * NB);
     const rsrc_t xr = make_rsrc(a.x, (uint32_t)((long long)a.T * K * 2));
     const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows
+    const int sc_part = tid / n_sc, sc_piece = tid - sc_part * n_sc;
 
-    auto load_scales = [&](int item) {
+    // an item: tile, column block and how many are left with it
+    struct Item {
+        int tile, cb, left;
+    };
+    auto next_item = [&](Item i) {
+        const bool wrap = i.cb + 1 == cblocks;
+        return Item{i.left > 1 && wrap ? i.tile + 1 : i.tile, i.left > 1 ? (wrap ? 0 : i.cb + 1) : i.cb, i.left - 1};
+    };
+    auto load_scales = [&](const Item &i) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (item < end && tid < 4 * n_sc) {
-            const uint32_t tile = tile_at(s, item / cblocks);
-            const int part = tid / n_sc, i = tid - part * n_sc;
-            const size_t row = (size_t)tile_expert_of(tile) * 2 * a.m + (part >= 2 ? a.m : 0) +
-                               (item % cblocks) * 16;
-            const uint16_t *src = (part & 1) ? a.gu_z : a.gu_s;
-            v = reinterpret_cast<const uint4 *>(src + row * groups)[i];
+        if (tid < 4 * n_sc) {
+            const size_t row = (size_t)tile_expert_of(tile_at(s, i.tile)) * 2 * a.m + (sc_part >= 2 ? a.m : 0) + i.cb * 16;
+            const uint16_t *src = (sc_part & 1) ? a.gu_z : a.gu_s;
+            v = reinterpret_cast<const uint4 *>(src + row * groups)[sc_piece];
         }
         return v;
     };
-    // one step's weight loads: its resource and lane offsets, then one load per
-    // group and half
+    // one step's weight loads: its resource (empty past the last item) and lane
+    // offsets, then one load per group and half
     struct Source {
         rsrc_t rsrc;
         uint32_t lane[2];
         int b;
-        bool live;
     };
-    auto source = [&](int item, int b) {
-        const int i = min(item, end - 1);
-        const int c0 = (i % cblocks) * 16;
+    auto source = [&](const Item &i, int b) {
         Source q;
-        q.rsrc = make_rsrc(a.gu_q + (size_t)tile_expert_of(tile_at(s, i / cblocks)) * a.m * K,
-                           (uint32_t)a.m * (uint32_t)K);
-        q.lane[0] = wq_lane_off<G, TL>(c0 + r, lane, K);
-        q.lane[1] = wq_lane_off<G, TL>(a.m + c0 + r, lane, K);
+        q.rsrc = make_rsrc(uniform(a.gu_q + (size_t)tile_expert_of(tile_at(s, i.tile)) * a.m * K),
+                           i.left > 0 ? (uint32_t)a.m * (uint32_t)K : 0u);
+        q.lane[0] = wq_lane_off<G, TL>(i.cb * 16 + r, lane, K);
+        q.lane[1] = wq_lane_off<G, TL>(a.m + i.cb * 16 + r, lane, K);
         q.b = b;
-        q.live = item < end;
         return q;
     };
     auto load_weight = [&](const Source &q, int h, int j) {
         const int gi = wave + kUpWaves * (q.b * NB + j);
-        return load_frag<G, TL>(q.rsrc, gi < groups && q.live ? q.lane[h] + wq_group_off<G, TL>(gi) : kOutOfRange, 0);
+        return load_frag<G, TL>(q.rsrc, gi < groups ? q.lane[h] + wq_group_off<G, TL>(gi) : kFewPast, 0);
     };
 
-    uint4 sc = load_scales(it);
+    Item cur{uniform(first / cblocks), uniform(first % cblocks), count};
+    uint4 sc = load_scales(cur);
     Frag<G> w[2][NB];
     {
-        const Source q = source(it, 0);
+        const Source q = source(cur, 0);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
                 w[h][j] = load_weight(q, h, j);
+                keep_load_order();
+            }
     }
     if (tid < 4 * n_sc)
         s_sc[tid] = sc;
@@ -333,20 +355,19 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     uint4 xv[NB][W];
     int have = -1, buf = 0;
     f32x4 acc[2];
-    for (int b = 0; it < end;) {
-        const uint32_t tile = tile_at(s, it / cblocks);
+    for (int b = 0; cur.left > 0;) {
+        const uint32_t tile = tile_at(s, cur.tile);
         const int n = tile_rows_of(tile), start = tile_start_of(tile);
-        if (have != (it / cblocks) * batches + b) {
-            have = (it / cblocks) * batches + b;
-            const uint32_t xrow = r < n ? (s.row[start + r] >> 16) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2))
-                                        : kOutOfRange;
+        if (have != cur.tile * batches + b) {
+            have = cur.tile * batches + b;
+            // rows past the tile's repeat its last one (their sums are not stored)
+            const uint32_t xrow = (s.row[start + min(r, n - 1)] >> 16) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2));
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const int gi = wave + kUpWaves * (b * NB + j);
 #pragma unroll
                 for (int t = 0; t < W; ++t)
-                    xv[j][t] = load16(xr, r < n && gi < groups ? xrow + (uint32_t)(gi * G * 2 + t * 16)
-                                                               : kOutOfRange, 0);
+                    xv[j][t] = load16(xr, (gi < groups ? xrow + (uint32_t)(gi * G * 2) : kFewPast) + (uint32_t)(t * 16), 0);
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j)
@@ -355,11 +376,13 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
                     xv[j][t] = permute8(xv[j][t]);
         }
         const bool last = !MULTI || b == batches - 1;
-        const int nit = last ? it + 1 : it, nb = last ? 0 : b + 1;
+        const Item nit = last ? next_item(cur) : cur;
+        const int nb = last ? 0 : b + 1;
         if (!MULTI || b == 0) {
-            sc = load_scales(it + 1);
+            sc = load_scales(next_item(cur));
             acc[0] = acc[1] = f32x4{0, 0, 0, 0};
         }
+        keep_load_order();
         const Source q = source(nit, nb);
         const uint16_t *sl = reinterpret_cast<const uint16_t *>(s_sc + buf * 4 * n_sc) + r * groups;
 #pragma unroll
@@ -379,6 +402,7 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
                         part, 0, 0, 0);
                 acc[h] += sv * part;
                 w[h][j] = load_weight(q, h, j);        // the next step's, into the registers just read
+                keep_load_order();
             }
         }
         if (last) {
@@ -398,28 +422,27 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
                 }
                 const uint32_t at = s.row[start + i] & 0xFFFF;
                 const _Float16 hv = (_Float16)(gelu_tanh(g) * u);
-                a.h[(size_t)at * a.m + permuted_col((it % cblocks) * 16 + c)] = __builtin_bit_cast(uint16_t, hv);
+                a.h[(size_t)at * a.m + permuted_col(cur.cb * 16 + c)] = __builtin_bit_cast(uint16_t, hv);
             }
             buf ^= 1;
         }
-        it = nit;
+        cur = nit;
         b = nb;
     }
 }
 
-// down and the weighted sum. A unit is one half of m's groups for one tile;
-// a wave takes every sixteenth unit, with the next step's weights loaded into
-// each fragment's registers as soon as it has been used (MULTI: the half holds
-// more than one step's groups). The scales of the tile's 16 rows are contiguous:
-// one 16-byte load per lane (NS of them past 16 groups) into the wave's own
-// slot of LDS.
-template <int G, bool TL, int NS, bool MULTI>
+// down and the weighted sum. A wave takes every sixteenth tile, m in steps of
+// NB groups; the next step's weights and activations are loaded into each
+// fragment's registers as soon as it has been used. The scales of the tile's
+// 16 weight rows are contiguous: one 16-byte load per lane (NS of them past 16
+// groups) into the wave's own slot of LDS.
+template <int G, bool TL, int NS>
 __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
     constexpr int NB = kBatch<G>, W = G / 32;
     __shared__ FewTiles s;
     __shared__ float s_w[kFewMaxAssign];
-    extern __shared__ uint4 s_dyn[];     // scales [waves][64 * NS], then Y [2][A][16] fp32
+    extern __shared__ uint4 s_dyn[];     // scales [waves][64 * NS], then Y [A][16] fp32
     const int lane = threadIdx.x & 63;
     const int wave = uniform((int)threadIdx.x >> 6);
     const int r = lane & 15, p = lane >> 4;
@@ -432,13 +455,12 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
         s_w[threadIdx.x] = a.w[threadIdx.x];
     build_tiles(s, a.ids, a.A, a.topk, a.E);
     const rsrc_t hr = make_rsrc(a.h, (uint32_t)((long long)a.A * K * 2));
-    const int half_groups = (groups + 1) / 2;
-    const int batches = (half_groups + NB - 1) / NB;
-    const int units = uniform(s.tiles) * 2;
+    const int batches = (groups + NB - 1) / NB;
+    const int tiles = uniform(s.tiles);
     const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows (z's follow from 32 NS)
 
-    auto load_scales = [&](uint4 (&v)[NS], int unit) {
-        const size_t row = (size_t)tile_expert_of(tile_at(s, min(unit, units - 1) >> 1)) * a.d + cb * 16;
+    auto load_scales = [&](uint4 (&v)[NS], int i0) {
+        const size_t row = (size_t)tile_expert_of(tile_at(s, min(i0, tiles - 1))) * a.d + cb * 16;
         const uint16_t *sp = a.dn_s + row * groups, *zp = a.dn_z + row * groups;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
@@ -447,88 +469,96 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
             v[i] = reinterpret_cast<const uint4 *>(z ? zp : sp)[min(z ? at - 32 * NS : at, n_sc - 1)];
         }
     };
+    // one step's weights and activations: rows past the tile's repeat its last
+    // one (their sums are not stored); past the last group both read zero
     struct Source {
         rsrc_t rsrc;
-        uint32_t lane;
-        int g0, g1;
+        uint32_t w, h;
+        int left;
     };
-    // the groups of one step and where its weights are; none past the last unit
-    auto source = [&](int unit, int b) {
-        const int u = min(unit, units - 1);
+    const uint32_t wo = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
+    auto source = [&](int i0, int b) {
+        const uint32_t tile = tile_at(s, min(i0, tiles - 1));
         Source q;
-        q.rsrc = make_rsrc(a.dn_q + (size_t)tile_expert_of(tile_at(s, u >> 1)) * a.d * (K / 2),
-                           (uint32_t)a.d * (uint32_t)(K / 2));
-        q.lane = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
-        q.g1 = unit < units ? ((u & 1) ? groups : half_groups) : 0;
-        q.g0 = (u & 1) * half_groups + b * NB;
+        q.rsrc = make_rsrc(uniform(a.dn_q + (size_t)tile_expert_of(tile) * a.d * (K / 2)),
+                           i0 < tiles ? (uint32_t)a.d * (uint32_t)(K / 2) : 0u);
+        q.w = wo + (uint32_t)b * wq_group_off<G, TL>(NB);
+        q.h = (s.row[tile_start_of(tile) + min(r, tile_rows_of(tile) - 1)] & 0xFFFF) * (uint32_t)(K * 2) +
+              (uint32_t)(p * (G / 2) + b * NB * G * 2);
+        q.left = groups - b * NB;
         return q;
     };
     auto load_weight = [&](const Source &q, int j) {
-        const int gi = q.g0 + j;
-        return load_frag<G, TL>(q.rsrc, gi < q.g1 ? q.lane + wq_group_off<G, TL>(gi) : kOutOfRange, 0);
+        return load_frag<G, TL>(q.rsrc, j < q.left ? q.w + wq_group_off<G, TL>(j) : kFewPast, 0);
+    };
+    auto load_h = [&](const Source &q, int j, int t) {
+        return load16(hr, (j < q.left ? q.h : kFewPast) + (uint32_t)(j * G * 2 + t * 16), 0);
     };
 
-    if (wave < units) {
+    if (wave < tiles) {
         uint4 sc[NS];
         Frag<G> w[NB];
+        uint4 hv[NB][W];
         load_scales(sc, wave);
-        Source cur = source(wave, 0);
+        keep_load_order();
+        {
+            const Source q = source(wave, 0);
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-            w[j] = load_weight(cur, j);
-        f32x4 acc = {0, 0, 0, 0};
-        for (int u = wave, b = 0; u < units;) {
-            const uint32_t tile = tile_at(s, u >> 1);
-            const int n = tile_rows_of(tile), start = tile_start_of(tile);
-            const uint32_t hrow = (s.row[start + min(r, n - 1)] & 0xFFFF) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2));
-            uint4 hv[NB][W];
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int j = 0; j < NB; ++j) {
+                w[j] = load_weight(q, j);
 #pragma unroll
                 for (int t = 0; t < W; ++t)
-                    hv[j][t] = load16(hr, r < n && cur.g0 + j < cur.g1
-                                              ? hrow + (uint32_t)((cur.g0 + j) * G * 2 + t * 16) : kOutOfRange, 0);
-            const bool last = !MULTI || b == batches - 1;
-            const int nu = last ? u + kDownWaves : u, nb = last ? 0 : b + 1;
-            if (!MULTI || b == 0) {
+                    hv[j][t] = load_h(q, j, t);
+                keep_load_order();
+            }
+        }
+        f32x4 acc = {0, 0, 0, 0};
+        for (int i0 = wave, b = 0; i0 < tiles;) {
+            const bool last = b == batches - 1;
+            const int ni = last ? i0 + kDownWaves : i0, nb = last ? 0 : b + 1;
+            const Source q = source(ni, nb);
+            if (b == 0) {
                 // the wave's own LDS slot: its earlier reads are done, in order
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
                     sc_lds[lane + 64 * i] = sc[i];
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
-                load_scales(sc, u + kDownWaves);
                 acc = f32x4{0, 0, 0, 0};
             }
-            const Source next = source(nu, nb);
+            load_scales(sc, ni);
+            keep_load_order();
             const uint16_t *sl = reinterpret_cast<const uint16_t *>(sc_lds) + r * groups;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 // past the last group: h is zero there, and the scale a finite one
-                const int gi = min(cur.g0 + j, groups - 1);
+                const int gi = min(b * NB + j, groups - 1);
                 f16x2 c1024, c64;
                 zero_point_consts(sl[32 * NS * 8 + gi], c1024, c64);
                 const float sv = (float)__builtin_bit_cast(_Float16, sl[gi]);
                 f32x4 part = {0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < W; ++t)
+                for (int t = 0; t < W; ++t) {
                     part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                         __builtin_bit_cast(f16x8, hv[j][t]), dequant8(frag_word<G>(w[j], t), c1024, c64),
                         part, 0, 0, 0);
+                    hv[j][t] = load_h(q, j, t);
+                }
+                w[j] = load_weight(q, j);
+                keep_load_order();
                 acc += sv * part;
-                w[j] = load_weight(next, j);       // the next step's, into the registers just read
             }
             if (last) {
-                float *y = s_y + (u & 1) * a.A * 16;
+                const uint32_t tile = tile_at(s, i0);
+                const int n = tile_rows_of(tile), start = tile_start_of(tile);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (4 * p + i < n)
-                        y[(s.row[start + 4 * p + i] & 0xFFFF) * 16 + r] = acc[i];
+                        s_y[(s.row[start + 4 * p + i] & 0xFFFF) * 16 + r] = acc[i];
                 __builtin_amdgcn_wave_barrier();
             }
-            u = nu;
+            i0 = ni;
             b = nb;
-            cur = next;
         }
     }
     __syncthreads();
@@ -538,10 +568,163 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
         for (int k = 0; k < a.topk; ++k) {
             const int at = t * a.topk + k;
             if (s.id[at] >= 0)
-                v = __fadd_rn(v, __fmul_rn(s_w[at], __fadd_rn(s_y[at * 16 + c], s_y[(a.A + at) * 16 + c])));
+                v = __fadd_rn(v, __fmul_rn(s_w[at], s_y[at * 16 + c]));
         }
         a.out[(size_t)t * a.d + cb * 16 + c] = __builtin_bit_cast(uint16_t, (_Float16)v);
     }
+}
+
+// down for more assignments: Y[a, :] = H[a] Wd_e^T in fp32, to be weighted and
+// summed by few_combine_kernel. The (tile, 16 columns) items are dealt to the
+// workgroups in contiguous runs. A workgroup takes its run tile by tile: the
+// tile's activations go to LDS (rows 16 bytes off the bank period), then its
+// waves take the tile's column blocks in turn, each streaming all of m past
+// them with the next step's weights loaded as soon as a fragment is used.
+template <int G, bool TL, int NS, bool MULTI>
+__global__ void __launch_bounds__(kUpThreads, 4) few_down_items_kernel(FewArgs a)
+{
+    constexpr int NB = kItemBatch<G>, W = G / 32;
+    __shared__ FewTiles s;
+    __shared__ uint4 s_sc[kUpWaves][64 * NS];
+    extern __shared__ __attribute__((aligned(16))) char s_h[];     // [16][2 m + 16]
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = uniform(tid >> 6);
+    const int r = lane & 15, p = lane >> 4;
+    const int K = a.m;
+    const int stride = K * 2 + 16;
+    const int groups = K / G;
+    const int cblocks = a.d / 16;
+    build_tiles(s, a.ids, a.A, a.topk, a.E);
+    const int items = uniform(s.tiles) * cblocks;
+    const int per = items / gridDim.x, rest = items % gridDim.x;
+    int at = uniform((int)blockIdx.x * per + min((int)blockIdx.x, rest));
+    const int end = uniform(at + per + ((int)blockIdx.x < rest ? 1 : 0));
+    const int batches = (groups + NB - 1) / NB;
+    const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows (z's follow from 32 NS)
+    const char *hp = s_h + r * stride + p * (G / 2);
+    const uint16_t *sl = reinterpret_cast<const uint16_t *>(s_sc[wave]) + r * groups;
+
+    for (int ti = at / cblocks; at < end; ++ti) {
+        const int c0 = uniform(at - ti * cblocks), c1 = uniform(min(cblocks, end - ti * cblocks));
+        at = ti * cblocks + c1;
+        const uint32_t tile = tile_at(s, ti);
+        const int n = tile_rows_of(tile), start = tile_start_of(tile);
+        const size_t e = (size_t)tile_expert_of(tile);
+        const uint8_t *wq = uniform(a.dn_q + e * a.d * (K / 2));
+        const uint16_t *sp = a.dn_s + e * a.d * groups, *zp = a.dn_z + e * a.d * groups;
+
+        // one step (a column block, NB groups): nothing is read past the last block
+        auto load_weight = [&](int c, int b, int j) {
+            const rsrc_t rs = make_rsrc(wq, c < c1 ? (uint32_t)a.d * (uint32_t)(K / 2) : 0u);
+            const uint32_t off = wq_lane_off<G, TL>(c * 16 + r, lane, K) + (uint32_t)b * wq_group_off<G, TL>(NB);
+            return load_frag<G, TL>(rs, b * NB + j < groups ? off + wq_group_off<G, TL>(j) : kFewPast, 0);
+        };
+        auto load_scales = [&](uint4 (&v)[NS], int c) {
+            const size_t row = (size_t)min(c, c1 - 1) * 16 * groups;
+#pragma unroll
+            for (int q = 0; q < NS; ++q) {
+                const int i = lane + 64 * q;
+                const bool z = i >= 32 * NS;
+                v[q] = reinterpret_cast<const uint4 *>((z ? zp : sp) + row)[min(z ? i - 32 * NS : i, n_sc - 1)];
+            }
+        };
+        uint4 sc[NS];
+        Frag<G> w[NB];
+        load_scales(sc, c0 + wave);
+        keep_load_order();
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            w[j] = load_weight(c0 + wave, 0, j);
+            keep_load_order();
+        }
+        // the tile's rows; those past n keep what they hold (their sums are not stored)
+        const int pieces = K / 8;
+        for (int i = tid; i < n * pieces; i += kUpThreads) {
+            const int row = i / pieces, c = i - row * pieces;
+            const uint32_t src = s.row[start + row] & 0xFFFF;
+            *reinterpret_cast<uint4 *>(s_h + row * stride + c * 16) =
+                *reinterpret_cast<const uint4 *>(a.h + (size_t)src * K + c * 8);
+        }
+        __syncthreads();
+        f32x4 acc = {0, 0, 0, 0};
+        for (int c = c0 + wave, b = 0; c < c1;) {
+            const bool last = !MULTI || b == batches - 1;
+            const int nc = last ? c + kUpWaves : c, nb = last ? 0 : b + 1;
+            if (!MULTI || b == 0) {
+                // the wave's own LDS slot: its earlier reads are done, in order
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    s_sc[wave][lane + 64 * i] = sc[i];
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                acc = f32x4{0, 0, 0, 0};
+            }
+            load_scales(sc, nc);
+            keep_load_order();
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                // past the last group the scale is 0 and the rest in range
+                const int gi = MULTI ? min(b * NB + j, groups - 1) : min(j, groups - 1);
+                const bool in = MULTI ? b * NB + j < groups : j < groups;
+                f16x2 c1024, c64;
+                zero_point_consts(sl[32 * NS * 8 + gi], c1024, c64);
+                const float sv = in ? (float)__builtin_bit_cast(_Float16, sl[gi]) : 0.0f;
+                f32x4 part = {0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        *reinterpret_cast<const f16x8 *>(hp + gi * (G * 2) + t * 16),
+                        dequant8(frag_word<G>(w[j], t), c1024, c64), part, 0, 0, 0);
+                w[j] = load_weight(nc, nb, j);    // the next step's, into the registers just read
+                keep_load_order();
+                if (in)
+                    acc += sv * part;
+            }
+            if (last) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * p + i < n)
+                        a.y[(size_t)(s.row[start + 4 * p + i] & 0xFFFF) * a.d + c * 16 + r] = acc[i];
+                __builtin_amdgcn_wave_barrier();
+            }
+            c = nc;
+            b = nb;
+        }
+        __syncthreads();                 // the next tile's rows replace these
+    }
+}
+
+// out[t, c] = sum_k w[t, k] Y[t topk + k, c], k ascending, four columns a thread.
+__global__ void __launch_bounds__(256) few_combine_kernel(FewArgs a)
+{
+    const int t = blockIdx.y, c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4;
+    if (c >= a.d)
+        return;
+    const float *y = a.y + (size_t)t * a.topk * a.d + c;
+    f32x4 v = {0, 0, 0, 0};
+    for (int k0 = 0; k0 < a.topk; k0 += 8) {
+        // eight choices' loads before the first addition; a dead one's slot is
+        // read with the others and left out of the sum
+        f32x4 yk[8];
+        float wk[8];
+        bool live[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int at = min(k0 + k, a.topk - 1);
+            const int id = a.ids[t * a.topk + at];
+            live[k] = k0 + k < a.topk && id >= 0 && id < a.E;
+            wk[k] = a.w[t * a.topk + at];
+            yk[k] = *reinterpret_cast<const f32x4 *>(y + (size_t)at * a.d);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (live[k])
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = __fadd_rn(v[i], __fmul_rn(wk[k], yk[k][i]));
+    }
+    *reinterpret_cast<uint2 *>(a.out + (size_t)t * a.d + c) = pack_f16x4(v);
 }
 
 template <int G, bool TL>
@@ -562,25 +745,46 @@ hipError_t run_gate_up(const FewArgs &a, bool routed, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int G, bool TL, int NS, bool MULTI>
+template <int G, bool TL, int NS>
 hipError_t run_down(const FewArgs &a, hipStream_t st)
 {
     static size_t allowed = 32 * 1024;
-    const size_t lds = (size_t)kDownWaves * 64 * NS * 16 + (size_t)a.A * 2 * 64;
-    const hipError_t err = allow_lds(few_down_kernel<G, TL, NS, MULTI>, lds, allowed);
+    const size_t lds = (size_t)kDownWaves * 64 * NS * 16 + (size_t)a.A * 64;
+    const hipError_t err = allow_lds(few_down_kernel<G, TL, NS>, lds, allowed);
     if (err != hipSuccess)
         return err;
-    few_down_kernel<G, TL, NS, MULTI><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
+    few_down_kernel<G, TL, NS><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int G, bool TL, int NS, bool MULTI>
+hipError_t run_down_items(const FewArgs &a, hipStream_t st)
+{
+    static size_t allowed = 32 * 1024;
+    const size_t lds = 16 * (2 * (size_t)a.m + 16);
+    hipError_t err = allow_lds(few_down_items_kernel<G, TL, NS, MULTI>, lds, allowed);
+    if (err != hipSuccess)
+        return err;
+    const int items = a.A * (a.d / 16);
+    const int groups = (items + kUpWaves - 1) / kUpWaves;
+    few_down_items_kernel<G, TL, NS, MULTI><<<dim3(groups < DGRID ? groups : DGRID), dim3(kUpThreads), lds, st>>>(a);
+    err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    few_combine_kernel<<<dim3((a.d / 4 + 255) / 256, a.T), dim3(256), 0, st>>>(a);
     return hipGetLastError();
 }
 
 template <int G, bool TL>
 hipError_t pick_down(const FewArgs &a, hipStream_t st)
 {
-    const int groups = a.m / G;
-    if (groups <= 2 * kBatch<G>)
-        return run_down<G, TL, 1, false>(a, st);
-    return groups <= 16 ? run_down<G, TL, 1, true>(a, st) : run_down<G, TL, 2, true>(a, st);
+    if (a.y != nullptr) {
+        const int groups = a.m / G;
+        if (groups <= kItemBatch<G>)
+            return run_down_items<G, TL, 1, false>(a, st);
+        return groups <= 16 ? run_down_items<G, TL, 1, true>(a, st) : run_down_items<G, TL, 2, true>(a, st);
+    }
+    return a.m / G <= 16 ? run_down<G, TL, 1>(a, st) : run_down<G, TL, 2>(a, st);
 }
 
 }  // namespace
@@ -589,6 +793,8 @@ bool few_routes_inside(int T, int topk, int E)
 {
     return T * topk <= kSmallAssign && E <= kFewRouteExperts;
 }
+
+bool few_keeps_outputs(int A) { return A > kFewSumInside; }
 
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream)
 {
