@@ -29,9 +29,6 @@
 namespace dgw4 {
 namespace {
 
-#ifndef DGRID
-#define DGRID 512
-#endif
 constexpr int kUpThreads = 512, kUpWaves = kUpThreads / 64;
 constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / 64;
 constexpr int kSmallAssign = 64;         // assignments that one wave sorts
@@ -201,10 +198,10 @@ __device__ inline uint32_t wave_max(uint32_t v)
 // One token's choices by one wave: dgw4_router's ids and weights. Lane l holds
 // the logits of experts l + 64 j; each round takes the largest key (the
 // logit's bits in order, see router_keys.hpp), among equal ones the lowest id.
+template <int PER>
 __device__ inline void route_token(const float *__restrict__ l, int E, int topk, int32_t *ids_lds,
                                    int32_t *__restrict__ ids, float *__restrict__ w, bool publish)
 {
-    constexpr int PER = kFewRouteExperts / 64;
     const int lane = threadIdx.x & 63;
     float v[PER];
     uint32_t key[PER];
@@ -279,9 +276,15 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     const int groups = K / G;
     const int cblocks = a.m / 16;
     if constexpr (ROUTED) {
-        for (int t = wave; t < a.T; t += kUpWaves)
-            route_token(a.logits + (size_t)t * a.E, a.E, a.topk, s.id + t * a.topk, a.rids + t * a.topk,
-                        a.rw + t * a.topk, blockIdx.x == 0);
+        for (int t = wave; t < a.T; t += kUpWaves) {
+            const float *l = a.logits + (size_t)t * a.E;
+            int32_t *ids = a.rids + t * a.topk;
+            float *w = a.rw + t * a.topk;
+            if (a.E <= 128)
+                route_token<2>(l, a.E, a.topk, s.id + t * a.topk, ids, w, blockIdx.x == 0);
+            else
+                route_token<kFewRouteExperts / 64>(l, a.E, a.topk, s.id + t * a.topk, ids, w, blockIdx.x == 0);
+        }
         __syncthreads();
         build_tiles_small(s, a.A, a.topk);
     } else {
@@ -336,8 +339,34 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
         return load_frag<G, TL>(q.rsrc, gi < groups ? q.lane[h] + wq_group_off<G, TL>(gi) : kFewPast, 0);
     };
 
+    // batch b of the tile's activations, then their order that of the weights;
+    // rows past the tile's repeat its last one (their sums are not stored)
+    uint4 xv[NB][W];
+    auto load_x = [&](uint32_t tile, int b) {
+        const int row = tile_start_of(tile) + min(r, tile_rows_of(tile) - 1);
+        const uint32_t xrow = (s.row[row] >> 16) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int gi = wave + kUpWaves * (b * NB + j);
+#pragma unroll
+            for (int t = 0; t < W; ++t)
+                xv[j][t] = load16(xr, (gi < groups ? xrow + (uint32_t)(gi * G * 2) : kFewPast) + (uint32_t)(t * 16), 0);
+        }
+    };
+    auto permute_x = [&]() {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int t = 0; t < W; ++t)
+                xv[j][t] = permute8(xv[j][t]);
+    };
+
     Item cur{uniform(first / cblocks), uniform(first % cblocks), count};
     uint4 sc = load_scales(cur);
+    keep_load_order();
+    int have = cur.tile * batches;
+    load_x(tile_at(s, cur.tile), 0);
+    keep_load_order();
     Frag<G> w[2][NB];
     {
         const Source q = source(cur, 0);
@@ -351,29 +380,17 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     }
     if (tid < 4 * n_sc)
         s_sc[tid] = sc;
+    permute_x();
     __syncthreads();
-    uint4 xv[NB][W];
-    int have = -1, buf = 0;
+    int buf = 0;
     f32x4 acc[2];
     for (int b = 0; cur.left > 0;) {
         const uint32_t tile = tile_at(s, cur.tile);
         const int n = tile_rows_of(tile), start = tile_start_of(tile);
         if (have != cur.tile * batches + b) {
             have = cur.tile * batches + b;
-            // rows past the tile's repeat its last one (their sums are not stored)
-            const uint32_t xrow = (s.row[start + min(r, n - 1)] >> 16) * (uint32_t)(K * 2) + (uint32_t)(p * (G / 2));
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int gi = wave + kUpWaves * (b * NB + j);
-#pragma unroll
-                for (int t = 0; t < W; ++t)
-                    xv[j][t] = load16(xr, (gi < groups ? xrow + (uint32_t)(gi * G * 2) : kFewPast) + (uint32_t)(t * 16), 0);
-            }
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int t = 0; t < W; ++t)
-                    xv[j][t] = permute8(xv[j][t]);
+            load_x(tile, b);
+            permute_x();
         }
         const bool last = !MULTI || b == batches - 1;
         const Item nit = last ? next_item(cur) : cur;
@@ -431,36 +448,41 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     }
 }
 
-// down and the weighted sum. A wave takes every sixteenth tile, m in steps of
-// NB groups; the next step's weights and activations are loaded into each
-// fragment's registers as soon as it has been used. The scales of the tile's
-// 16 weight rows are contiguous: one 16-byte load per lane (NS of them past 16
-// groups) into the wave's own slot of LDS.
+// down and the weighted sum, for the fewest assignments. All of H goes to LDS
+// (rows 16 bytes off the bank period) while the first weights are on their way.
+// A unit is one half of m's groups for one tile; a wave takes every sixteenth
+// unit, in steps of NB groups, the next step's weights loaded into each
+// fragment's registers as soon as it has been used. (One token's eight tiles
+// are sixteen units: every load of the kernel goes out at once.) The scales of
+// the tile's 16 weight rows are contiguous: one 16-byte load per lane (NS of
+// them past 16 groups) into the wave's own slot of LDS.
 template <int G, bool TL, int NS>
 __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
     constexpr int NB = kBatch<G>, W = G / 32;
     __shared__ FewTiles s;
-    __shared__ float s_w[kFewMaxAssign];
-    extern __shared__ uint4 s_dyn[];     // scales [waves][64 * NS], then Y [A][16] fp32
-    const int lane = threadIdx.x & 63;
-    const int wave = uniform((int)threadIdx.x >> 6);
+    __shared__ float s_w[kFewSumInside];
+    __shared__ float s_y[2][kFewSumInside][16];
+    __shared__ uint4 s_sc[kDownWaves][64 * NS];
+    extern __shared__ __attribute__((aligned(16))) char s_h[];     // [A][2 m + 16]
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = uniform(tid >> 6);
     const int r = lane & 15, p = lane >> 4;
     const int K = a.m;
+    const int stride = K * 2 + 16;
     const int groups = K / G;
     const int cb = blockIdx.x;
-    uint4 *sc_lds = s_dyn + wave * 64 * NS;
-    float *s_y = reinterpret_cast<float *>(s_dyn + kDownWaves * 64 * NS);
-    if ((int)threadIdx.x < a.A)
-        s_w[threadIdx.x] = a.w[threadIdx.x];
+    if (tid < a.A)
+        s_w[tid] = a.w[tid];
     build_tiles(s, a.ids, a.A, a.topk, a.E);
-    const rsrc_t hr = make_rsrc(a.h, (uint32_t)((long long)a.A * K * 2));
-    const int batches = (groups + NB - 1) / NB;
-    const int tiles = uniform(s.tiles);
+    const int half_groups = (groups + 1) / 2;
+    const int batches = (half_groups + NB - 1) / NB;
+    const int units = uniform(s.tiles) * 2;
     const int n_sc = 2 * groups;         // 16-byte pieces of one array's 16 rows (z's follow from 32 NS)
 
-    auto load_scales = [&](uint4 (&v)[NS], int i0) {
-        const size_t row = (size_t)tile_expert_of(tile_at(s, min(i0, tiles - 1))) * a.d + cb * 16;
+    auto load_scales = [&](uint4 (&v)[NS], int u) {
+        const size_t row = (size_t)tile_expert_of(tile_at(s, min(u, units - 1) >> 1)) * a.d + cb * 16;
         const uint16_t *sp = a.dn_s + row * groups, *zp = a.dn_z + row * groups;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
@@ -469,106 +491,108 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
             v[i] = reinterpret_cast<const uint4 *>(z ? zp : sp)[min(z ? at - 32 * NS : at, n_sc - 1)];
         }
     };
-    // one step's weights and activations: rows past the tile's repeat its last
-    // one (their sums are not stored); past the last group both read zero
+    // one step's weights (zero past the half's last group)
     struct Source {
         rsrc_t rsrc;
-        uint32_t w, h;
-        int left;
+        uint32_t w;
+        int left, g0;
     };
     const uint32_t wo = wq_lane_off<G, TL>(cb * 16 + r, lane, K);
-    auto source = [&](int i0, int b) {
-        const uint32_t tile = tile_at(s, min(i0, tiles - 1));
+    auto source = [&](int u, int b) {
         Source q;
-        q.rsrc = make_rsrc(uniform(a.dn_q + (size_t)tile_expert_of(tile) * a.d * (K / 2)),
-                           i0 < tiles ? (uint32_t)a.d * (uint32_t)(K / 2) : 0u);
-        q.w = wo + (uint32_t)b * wq_group_off<G, TL>(NB);
-        q.h = (s.row[tile_start_of(tile) + min(r, tile_rows_of(tile) - 1)] & 0xFFFF) * (uint32_t)(K * 2) +
-              (uint32_t)(p * (G / 2) + b * NB * G * 2);
-        q.left = groups - b * NB;
+        q.rsrc = make_rsrc(uniform(a.dn_q + (size_t)tile_expert_of(tile_at(s, min(u, units - 1) >> 1)) * a.d * (K / 2)),
+                           u < units ? (uint32_t)a.d * (uint32_t)(K / 2) : 0u);
+        q.g0 = (u & 1) * half_groups + b * NB;
+        q.w = wo + wq_group_off<G, TL>(q.g0);
+        q.left = ((u & 1) ? groups : half_groups) - q.g0;
         return q;
     };
     auto load_weight = [&](const Source &q, int j) {
         return load_frag<G, TL>(q.rsrc, j < q.left ? q.w + wq_group_off<G, TL>(j) : kFewPast, 0);
     };
-    auto load_h = [&](const Source &q, int j, int t) {
-        return load16(hr, (j < q.left ? q.h : kFewPast) + (uint32_t)(j * G * 2 + t * 16), 0);
-    };
 
-    if (wave < tiles) {
-        uint4 sc[NS];
-        Frag<G> w[NB];
-        uint4 hv[NB][W];
+    uint4 sc[NS];
+    Frag<G> w[NB];
+    Source cur{};
+    if (units > 0) {
         load_scales(sc, wave);
         keep_load_order();
-        {
-            const Source q = source(wave, 0);
+        cur = source(wave, 0);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                w[j] = load_weight(q, j);
-#pragma unroll
-                for (int t = 0; t < W; ++t)
-                    hv[j][t] = load_h(q, j, t);
-                keep_load_order();
-            }
-        }
-        f32x4 acc = {0, 0, 0, 0};
-        for (int i0 = wave, b = 0; i0 < tiles;) {
-            const bool last = b == batches - 1;
-            const int ni = last ? i0 + kDownWaves : i0, nb = last ? 0 : b + 1;
-            const Source q = source(ni, nb);
-            if (b == 0) {
-                // the wave's own LDS slot: its earlier reads are done, in order
-#pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    sc_lds[lane + 64 * i] = sc[i];
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                acc = f32x4{0, 0, 0, 0};
-            }
-            load_scales(sc, ni);
+        for (int j = 0; j < NB; ++j) {
+            w[j] = load_weight(cur, j);
             keep_load_order();
-            const uint16_t *sl = reinterpret_cast<const uint16_t *>(sc_lds) + r * groups;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                // past the last group: h is zero there, and the scale a finite one
-                const int gi = min(b * NB + j, groups - 1);
-                f16x2 c1024, c64;
-                zero_point_consts(sl[32 * NS * 8 + gi], c1024, c64);
-                const float sv = (float)__builtin_bit_cast(_Float16, sl[gi]);
-                f32x4 part = {0, 0, 0, 0};
-#pragma unroll
-                for (int t = 0; t < W; ++t) {
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        __builtin_bit_cast(f16x8, hv[j][t]), dequant8(frag_word<G>(w[j], t), c1024, c64),
-                        part, 0, 0, 0);
-                    hv[j][t] = load_h(q, j, t);
-                }
-                w[j] = load_weight(q, j);
-                keep_load_order();
-                acc += sv * part;
-            }
-            if (last) {
-                const uint32_t tile = tile_at(s, i0);
-                const int n = tile_rows_of(tile), start = tile_start_of(tile);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * p + i < n)
-                        s_y[(s.row[start + 4 * p + i] & 0xFFFF) * 16 + r] = acc[i];
-                __builtin_amdgcn_wave_barrier();
-            }
-            i0 = ni;
-            b = nb;
         }
     }
+    const int pieces = K / 8;
+    for (int i = tid; i < a.A * pieces; i += kDownThreads) {
+        const int row = i / pieces, c = i - row * pieces;
+        // a dead assignment's row was never written: not read either
+        if (s.id[row] >= 0)
+            *reinterpret_cast<uint4 *>(s_h + row * stride + c * 16) =
+                *reinterpret_cast<const uint4 *>(a.h + (size_t)row * K + c * 8);
+    }
     __syncthreads();
-    for (int o = threadIdx.x; o < a.T * 16; o += kDownThreads) {
-        const int t = o >> 4, c = o & 15;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int u = wave, b = 0; u < units;) {
+        const bool last = b == batches - 1;
+        const int nu = last ? u + kDownWaves : u, nb = last ? 0 : b + 1;
+        const Source q = source(nu, nb);
+        const uint32_t tile = tile_at(s, u >> 1);
+        const int n = tile_rows_of(tile), start = tile_start_of(tile);
+        // rows past the tile's repeat its last one (their sums are not stored)
+        const char *hp = s_h + (s.row[start + min(r, n - 1)] & 0xFFFF) * stride + p * (G / 2);
+        if (b == 0) {
+            // the wave's own LDS slot: its earlier reads are done, in order
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                s_sc[wave][lane + 64 * i] = sc[i];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            acc = f32x4{0, 0, 0, 0};
+        }
+        load_scales(sc, nu);
+        keep_load_order();
+        const uint16_t *sl = reinterpret_cast<const uint16_t *>(s_sc[wave]) + r * groups;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            // past the half's last group: left out
+            const int gi = min(cur.g0 + j, groups - 1);
+            const bool in = j < cur.left;
+            f16x2 c1024, c64;
+            zero_point_consts(sl[32 * NS * 8 + gi], c1024, c64);
+            const float sv = (float)__builtin_bit_cast(_Float16, sl[gi]);
+            f32x4 part = {0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < W; ++t)
+                part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    *reinterpret_cast<const f16x8 *>(hp + gi * (G * 2) + t * 16),
+                    dequant8(frag_word<G>(w[j], t), c1024, c64), part, 0, 0, 0);
+            w[j] = load_weight(q, j);
+            keep_load_order();
+            if (in)
+                acc += sv * part;
+        }
+        if (last) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * p + i < n)
+                    s_y[u & 1][s.row[start + 4 * p + i] & 0xFFFF][r] = acc[i];
+            __builtin_amdgcn_wave_barrier();
+        }
+        u = nu;
+        b = nb;
+        cur = q;
+    }
+    __syncthreads();
+    // T * topk <= 16: one thread per output
+    if (tid < a.T * 16) {
+        const int t = tid >> 4, c = tid & 15;
         float v = 0.f;
         for (int k = 0; k < a.topk; ++k) {
             const int at = t * a.topk + k;
             if (s.id[at] >= 0)
-                v = __fadd_rn(v, __fmul_rn(s_w[at], s_y[at * 16 + c]));
+                v = __fadd_rn(v, __fmul_rn(s_w[at], __fadd_rn(s_y[0][at][c], s_y[1][at][c])));
         }
         a.out[(size_t)t * a.d + cb * 16 + c] = __builtin_bit_cast(uint16_t, (_Float16)v);
     }
@@ -748,8 +772,8 @@ hipError_t run_gate_up(const FewArgs &a, bool routed, hipStream_t st)
 template <int G, bool TL, int NS>
 hipError_t run_down(const FewArgs &a, hipStream_t st)
 {
-    static size_t allowed = 32 * 1024;
-    const size_t lds = (size_t)kDownWaves * 64 * NS * 16 + (size_t)a.A * 64;
+    static size_t allowed = 24 * 1024;
+    const size_t lds = (size_t)a.A * (2 * (size_t)a.m + 16);
     const hipError_t err = allow_lds(few_down_kernel<G, TL, NS>, lds, allowed);
     if (err != hipSuccess)
         return err;
@@ -767,7 +791,7 @@ hipError_t run_down_items(const FewArgs &a, hipStream_t st)
         return err;
     const int items = a.A * (a.d / 16);
     const int groups = (items + kUpWaves - 1) / kUpWaves;
-    few_down_items_kernel<G, TL, NS, MULTI><<<dim3(groups < DGRID ? groups : DGRID), dim3(kUpThreads), lds, st>>>(a);
+    few_down_items_kernel<G, TL, NS, MULTI><<<dim3(groups < 512 ? groups : 512), dim3(kUpThreads), lds, st>>>(a);
     err = hipGetLastError();
     if (err != hipSuccess)
         return err;
