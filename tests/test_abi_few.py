@@ -76,11 +76,11 @@ def test_few_route_arguments():
 
 
 def test_few_workspace():
-    # the intermediate, the router's ids and weights, and past 16 assignments
-    # their outputs, each in whole 256 bytes
-    assert dg.moe_few_workspace_bytes(1, 8, 128, 2816, 704) == 8 * 704 * 2 + 2 * 256
-    assert dg.moe_few_workspace_bytes(64, 8, 128, 2816, 704) == 512 * 704 * 2 + 2 * 2048 + 512 * 2816 * 4
-    assert dg.moe_few_workspace_bytes(2, 8, 128, 2816, 704) == 16 * 704 * 2 + 2 * 256
+    # the intermediate, the router's ids and weights, the tile list, and past 64
+    # assignments their outputs, each in whole 256 bytes
+    assert dg.moe_few_workspace_bytes(1, 8, 128, 2816, 704) == 8 * 704 * 2 + 2 * 256 + 6400
+    assert dg.moe_few_workspace_bytes(8, 8, 128, 2816, 704) == 64 * 704 * 2 + 2 * 256 + 6400
+    assert dg.moe_few_workspace_bytes(64, 8, 128, 2816, 704) == 512 * 704 * 2 + 2 * 2048 + 6400 + 512 * 2816 * 4
     assert dg.moe_few_workspace_bytes(0, 8, 128, 2816, 704) == 0
     with pytest.raises(dg.Dgw4Error, match="UNSUPPORTED"):
         dg.moe_few_workspace_bytes(65, 8, 128, 2816, 704)

@@ -591,7 +591,8 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
     const size_t h_bytes = round_up(sizeof(uint16_t) * (size_t)A * (size_t)m);
     const size_t id_bytes = round_up(sizeof(int32_t) * (size_t)A);
     const size_t y_bytes = dgw4::few_keeps_outputs((int)A) ? sizeof(float) * (size_t)A * (size_t)d : 0;
-    const size_t need = h_bytes + 2 * id_bytes + round_up(y_bytes);
+    const size_t list_bytes = A > 0 ? round_up(dgw4::kFewListBytes) : 0;
+    const size_t need = h_bytes + 2 * id_bytes + list_bytes + round_up(y_bytes);
     if (!workspace) {
         *ws_bytes = need;
         return DGW4_OK;
@@ -629,7 +630,8 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
     a.gu_tiled = gu_tiled;
     a.dn_tiled = dn_tiled;
     a.h = reinterpret_cast<uint16_t *>(ws);
-    a.y = y_bytes ? reinterpret_cast<float *>(ws + h_bytes + 2 * id_bytes) : nullptr;
+    a.list = ws + h_bytes + 2 * id_bytes;
+    a.y = y_bytes ? reinterpret_cast<float *>(ws + h_bytes + 2 * id_bytes + list_bytes) : nullptr;
     a.out = out;
     if (routed) {
         int32_t *rids = reinterpret_cast<int32_t *>(ws + h_bytes);

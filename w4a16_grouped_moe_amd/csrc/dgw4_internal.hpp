@@ -141,6 +141,7 @@ hipError_t launch_mfma_probe(int iters, uint32_t *sink, double *flops, hipStream
 
 // The layer for few tokens (moe_few.hip): at most kFewMaxAssign assignments.
 constexpr int kFewMaxAssign = 512;
+constexpr int kFewListBytes = (1024 + kFewMaxAssign + 4) * 4;
 
 struct FewArgs {
     const uint16_t *x;          // fp16 [T, d]
@@ -156,13 +157,14 @@ struct FewArgs {
     const uint16_t *dn_s, *dn_z;
     int gu_tiled, dn_tiled;
     uint16_t *h;                // fp16 [A, m], columns permuted per 8 (workspace)
+    void *list;                 // kFewListBytes: the first launch's tile list (workspace)
     float *y;                   // fp32 [A, d], each assignment's output (workspace); null: kept in LDS
     uint16_t *out;              // fp16 [T, d]
 };
 
 // Up to this many assignments down weights and sums the experts' outputs
 // itself; with more, a third launch does (see moe_few.hip).
-constexpr int kFewSumInside = 16;
+constexpr int kFewSumInside = 64;
 bool few_keeps_outputs(int A);
 
 // The groups of d and of m the two kernels keep scales for.

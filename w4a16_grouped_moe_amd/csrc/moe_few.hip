@@ -16,8 +16,9 @@
 // that kernel keeps 16 of the 256 compute units busy.
 //
 // A tile is up to 16 assignments of one expert (one MFMA row block). Every
-// workgroup builds the list of tiles itself from the ids (no launch, no
-// global buffers). All workgroups agree on which assignments a tile holds: an
+// workgroup of the first launch builds the list of tiles itself from the ids
+// (no launch before it); its first workgroup leaves the list in the workspace
+// for the second launch. All workgroups agree on which assignments a tile holds: an
 // expert with up to 16 has one tile, whose row order is of no matter (each
 // MFMA row is a sum of its own in a fixed order of K); one with more takes its
 // assignments in ascending order, 16 to a tile.
@@ -42,15 +43,21 @@ constexpr int kBatch = G == 128 ? 3 : 6;
 template <int G>
 constexpr int kItemBatch = G == 128 ? 6 : 11;    // in few_down_items_kernel
 
-// The tile list of one workgroup: tile i holds the assignments row[start ..
-// start + n) (low half, their tokens in the high half).
-struct FewTiles {
+// The tile list: tile i holds the assignments row[start .. start + n) (low half,
+// their tokens in the high half).
+struct FewList {
     uint32_t row[16 * kSmallAssign];
     uint32_t tile[kFewMaxAssign];        // expert | start << 10 | n << 20
+    int tiles;
+    int pad[3];
+};
+static_assert(sizeof(FewList) == kFewListBytes && sizeof(FewList) % 16 == 0, "copied in 16-byte pieces");
+
+// One workgroup's list and what it is built with.
+struct FewTiles : FewList {
     int32_t id[kFewMaxAssign];           // each assignment's expert, -1 if none
     int count[kMaxExperts];              // assignments of each expert
     uint32_t base[kMaxExperts];          // first tile << 16 | first row of each expert
-    int tiles;
 };
 static_assert(16 * kSmallAssign >= kFewMaxAssign, "the row list holds either form");
 
@@ -69,7 +76,7 @@ __device__ inline const P *uniform(const P *p)
     return (const P *)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
-__device__ inline uint32_t tile_at(const FewTiles &s, int i) { return (uint32_t)uniform((int)s.tile[i]); }
+__device__ inline uint32_t tile_at(const FewList &s, int i) { return (uint32_t)uniform((int)s.tile[i]); }
 __device__ inline int tile_expert_of(uint32_t t) { return (int)(t & 0x3FF); }
 __device__ inline int tile_start_of(uint32_t t) { return (int)(t >> 10 & 0x3FF); }
 __device__ inline int tile_rows_of(uint32_t t) { return (int)(t >> 20); }
@@ -178,6 +185,20 @@ __device__ inline void build_tiles(FewTiles &s, const int32_t *__restrict__ ids,
         build_tiles_small(s, A, topk);
     else
         build_tiles_any(s, A, topk, E);
+}
+
+// The first launch's list for the second (building it again takes 1 to 2.2 us).
+__device__ inline void publish_list(const FewList &s, void *to)
+{
+    for (int i = threadIdx.x; i < (int)sizeof(FewList) / 16; i += blockDim.x)
+        static_cast<uint4 *>(to)[i] = reinterpret_cast<const uint4 *>(&s)[i];
+}
+
+__device__ inline void read_list(FewList &s, const void *from)
+{
+    for (int i = threadIdx.x; i < (int)sizeof(FewList) / 16; i += blockDim.x)
+        reinterpret_cast<uint4 *>(&s)[i] = static_cast<const uint4 *>(from)[i];
+    __syncthreads();
 }
 
 // The largest of a wave's values, in every lane: within rows of 16 lanes by
@@ -290,6 +311,8 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     } else {
         build_tiles(s, a.ids, a.A, a.topk, a.E);
     }
+    if (blockIdx.x == 0)
+        publish_list(s, a.list);
     const int items = uniform(s.tiles) * cblocks;
     const int per = items / gridDim.x, rest = items % gridDim.x;
     const int first = uniform((int)blockIdx.x * per + min((int)blockIdx.x, rest));
@@ -460,8 +483,9 @@ template <int G, bool TL, int NS>
 __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
     constexpr int NB = kBatch<G>, W = G / 32;
-    __shared__ FewTiles s;
+    __shared__ FewList s;
     __shared__ float s_w[kFewSumInside];
+    __shared__ bool s_live[kFewSumInside];
     __shared__ float s_y[2][kFewSumInside][16];
     __shared__ uint4 s_sc[kDownWaves][64 * NS];
     extern __shared__ __attribute__((aligned(16))) char s_h[];     // [A][2 m + 16]
@@ -473,9 +497,12 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
     const int stride = K * 2 + 16;
     const int groups = K / G;
     const int cb = blockIdx.x;
-    if (tid < a.A)
+    if (tid < a.A) {
+        const int id = a.ids[tid];
         s_w[tid] = a.w[tid];
-    build_tiles(s, a.ids, a.A, a.topk, a.E);
+        s_live[tid] = id >= 0 && id < a.E;
+    }
+    read_list(s, a.list);
     const int half_groups = (groups + 1) / 2;
     const int batches = (half_groups + NB - 1) / NB;
     const int units = uniform(s.tiles) * 2;
@@ -528,7 +555,7 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
     for (int i = tid; i < a.A * pieces; i += kDownThreads) {
         const int row = i / pieces, c = i - row * pieces;
         // a dead assignment's row was never written: not read either
-        if (s.id[row] >= 0)
+        if (s_live[row])
             *reinterpret_cast<uint4 *>(s_h + row * stride + c * 16) =
                 *reinterpret_cast<const uint4 *>(a.h + (size_t)row * K + c * 8);
     }
@@ -585,13 +612,13 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
         cur = q;
     }
     __syncthreads();
-    // T * topk <= 16: one thread per output
+    // T * topk <= 64: one thread per output
     if (tid < a.T * 16) {
         const int t = tid >> 4, c = tid & 15;
         float v = 0.f;
         for (int k = 0; k < a.topk; ++k) {
             const int at = t * a.topk + k;
-            if (s.id[at] >= 0)
+            if (s_live[at])
                 v = __fadd_rn(v, __fmul_rn(s_w[at], __fadd_rn(s_y[0][at][c], s_y[1][at][c])));
         }
         a.out[(size_t)t * a.d + cb * 16 + c] = __builtin_bit_cast(uint16_t, (_Float16)v);
@@ -608,7 +635,7 @@ template <int G, bool TL, int NS, bool MULTI>
 __global__ void __launch_bounds__(kUpThreads, 4) few_down_items_kernel(FewArgs a)
 {
     constexpr int NB = kItemBatch<G>, W = G / 32;
-    __shared__ FewTiles s;
+    __shared__ FewList s;
     __shared__ uint4 s_sc[kUpWaves][64 * NS];
     extern __shared__ __attribute__((aligned(16))) char s_h[];     // [16][2 m + 16]
     const int tid = threadIdx.x;
@@ -619,7 +646,7 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_down_items_kernel(FewArgs a
     const int stride = K * 2 + 16;
     const int groups = K / G;
     const int cblocks = a.d / 16;
-    build_tiles(s, a.ids, a.A, a.topk, a.E);
+    read_list(s, a.list);
     const int items = uniform(s.tiles) * cblocks;
     const int per = items / gridDim.x, rest = items % gridDim.x;
     int at = uniform((int)blockIdx.x * per + min((int)blockIdx.x, rest));
