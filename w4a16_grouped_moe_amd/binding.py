@@ -517,9 +517,11 @@ def moe_few_workspace_bytes(T: int, topk: int, E: int, d: int, m: int, gu_g: int
 
 
 # The entry points below run a few microseconds of GPU work per call, so their
-# host side is kept short: one integer per tensor for its device, the raw
-# stream handle, no context manager where the device is the current one.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# host side is kept short: one integer per tensor for its device, one condition
+# per tensor where all is well (the reason is looked for only when it is not),
+# the raw stream handle, no context manager where the device is the current one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def _gpu(t, name: str) -> int:
@@ -532,15 +534,20 @@ def _gpu(t, name: str) -> int:
     return d
 
 
-def _flat(t, name: str, dtypes, d: int) -> int:
-    """Pointer of a contiguous tensor on device d."""
+def _refuse(t, name: str, dtypes, d: int):
+    """Raises for a tensor of another device or type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != d:
         raise ValueError(f"{name} is on {t.device}, not on the ROCm device cuda:{d}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
-    if not t.is_contiguous():
+
+
+def _flat(t, name: str, dtypes, d: int) -> int:
+    """Pointer of a contiguous tensor on device d."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == d and t.dtype in dtypes and t.is_contiguous()):
+        _refuse(t, name, dtypes, d)
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -549,12 +556,11 @@ def _call(fn: str, d: int, *args) -> None:
     """Enqueue one call on device d's current stream, with that device the
     current one for the call."""
     f = getattr(_lib or lib(), fn)
-    st = _raw_stream(d) if _raw_stream else torch.cuda.current_stream(d).cuda_stream
     if torch.cuda.current_device() == d:
-        status = f(*args, st)
+        status = f(*args, _raw_stream(d))
     else:
         with torch.cuda.device(d):
-            status = f(*args, st)
+            status = f(*args, _raw_stream(d))
     if status != OK:
         raise Dgw4Error(fn, status)
 
@@ -628,15 +634,11 @@ def moe_few_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, gu: 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, d: int) -> tuple[int, int]:
-    """Pointer and row distance of a 2-d tensor on device d whose rows are
-    contiguous but may lie apart (a slice of a wider tensor)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != d:
-        raise ValueError(f"{name} is on {t.device}, not on the ROCm device cuda:{d}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+def _rows(t: torch.Tensor, name: str, dtypes, d: int) -> tuple[int, int, int, int]:
+    """Pointer, rows, columns and row distance of a 2-d tensor on device d whose
+    rows are contiguous but may lie apart (a slice of a wider tensor)."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == d and t.dtype in dtypes):
+        _refuse(t, name, dtypes, d)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
@@ -645,7 +647,7 @@ def _rows(t: torch.Tensor, name: str, dtypes, d: int) -> tuple[int, int]:
         ld = cols
     if (cols > 1 and step != 1) or ld < cols:
         raise ValueError(f"{name}: the elements of a row must be contiguous, its rows must not overlap")
-    return t.data_ptr(), ld
+    return t.data_ptr(), rows, cols, ld
 
 
 def _up16(k: int) -> int:
@@ -657,29 +659,33 @@ def quantize_rows_i8(x: torch.Tensor, out: tuple | None = None):
     [rows, K]; rows may lie apart): (q int8 [rows, K rounded up to 16], the
     added columns zero, s fp32 [rows]). ``out`` = (q, s) to write into."""
     d = _gpu(x, "x")
-    px, ldx = _rows(x, "x", _TYPES, d)
-    rows, K = x.shape
+    px, rows, K, ldx = _rows(x, "x", _TYPES, d)
     Kp = _up16(K)
     if out is None:
-        out = (torch.empty((rows, Kp), dtype=torch.int8, device=x.device),
-               torch.empty(rows, dtype=torch.float32, device=x.device))
-    q, s = out
-    if q.shape != (rows, Kp) or s.shape != (rows,):
-        raise ValueError("out must be (q [rows, K rounded up to 16], s [rows])")
-    pq, ldq = _rows(q, "q", _I8, d)
-    _call("dgw4_quantize_rows_i8", d, px, _TYPES[x.dtype], rows, K, ldx, pq, ldq,
-          _flat(s, "s", _F32, d))
+        q = x.new_empty((rows, Kp), dtype=torch.int8)
+        s = x.new_empty(rows, dtype=torch.float32)
+        pq, ldq, ps = q.data_ptr(), Kp, s.data_ptr()
+    else:
+        q, s = out
+        pq, q_rows, q_cols, ldq = _rows(q, "q", _I8, d)
+        ps = _flat(s, "s", _F32, d)
+        if (q_rows, q_cols) != (rows, Kp) or s.shape != (rows,):
+            raise ValueError("out must be (q [rows, K rounded up to 16], s [rows])")
+    _call("dgw4_quantize_rows_i8", d, px, _TYPES[x.dtype], rows, K, ldx, pq, ldq, ps)
     return q, s
 
 
-def _w8a8_out(x, N: int, dtype, out):
+def _w8a8_out(x, T: int, N: int, dtype, out, d: int):
+    """The output, its pointer and row distance."""
     if out is None:
         if dtype not in _TYPES:
             raise TypeError(f"dtype {dtype} not in {tuple(_TYPES)}")
-        return torch.empty((x.shape[0], N), dtype=dtype, device=x.device)
-    if out.shape != (x.shape[0], N):
+        out = x.new_empty((T, N), dtype=dtype)
+        return out, out.data_ptr(), N
+    py, rows, cols, ldy = _rows(out, "out", _TYPES, d)
+    if (rows, cols) != (T, N):
         raise ValueError("out must be [T, N]")
-    return out
+    return out, py, ldy
 
 
 def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
@@ -692,17 +698,14 @@ def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor 
     then. See dgw4_w8a8_linear in include/dgw4.h."""
     wq, ws = w
     d = _gpu(xq, "xq")
-    px, ldx = _rows(xq, "xq", _I8, d)
-    pw, ldw = _rows(wq, "wq", _I8, d)
-    T, K = xq.shape
-    N, Kw = wq.shape
+    px, T, K, ldx = _rows(xq, "xq", _I8, d)
+    pw, N, Kw, ldw = _rows(wq, "wq", _I8, d)
+    pxs, pws = _flat(xs, "xs", _F32, d), _flat(ws, "ws", _F32, d)
     if Kw != K or xs.shape != (T,) or ws.shape != (N,):
         raise ValueError(f"wq {tuple(wq.shape)}, xs {tuple(xs.shape)}, ws {tuple(ws.shape)} do not "
                          f"match xq {tuple(xq.shape)}")
-    out = _w8a8_out(xq, N, dtype, out)
-    py, ldy = _rows(out, "out", _TYPES, d)
-    _call("dgw4_w8a8_linear", d, px, _flat(xs, "xs", _F32, d), T, K, ldx, pw,
-          _flat(ws, "ws", _F32, d), N, ldw, py, _TYPES[out.dtype], ldy)
+    out, py, ldy = _w8a8_out(xq, T, N, dtype, out, d)
+    _call("dgw4_w8a8_linear", d, px, pxs, T, K, ldx, pw, pws, N, ldw, py, _TYPES[out.dtype], ldy)
     return out
 
 
@@ -724,17 +727,15 @@ def w8a8_linear_tokens(x: torch.Tensor, w: tuple, out: torch.Tensor | None = Non
     when not given."""
     wq, ws = w
     d = _gpu(x, "x")
-    px, ldx = _rows(x, "x", _TYPES, d)
-    pw, ldw = _rows(wq, "wq", _I8, d)
-    T, K = x.shape
-    N, Kw = wq.shape
+    px, T, K, ldx = _rows(x, "x", _TYPES, d)
+    pw, N, Kw, ldw = _rows(wq, "wq", _I8, d)
+    pws = _flat(ws, "ws", _F32, d)
     if Kw != _up16(K) or ws.shape != (N,):
         raise ValueError(f"wq {tuple(wq.shape)}, ws {tuple(ws.shape)} do not match x {tuple(x.shape)}")
-    out = _w8a8_out(x, N, dtype, out)
-    py, ldy = _rows(out, "out", _TYPES, d)
+    out, py, ldy = _w8a8_out(x, T, N, dtype, out, d)
     if workspace is None:
-        workspace = torch.empty(max(w8a8_workspace_bytes(T, K), 1), dtype=torch.uint8, device=x.device)
-    _call("dgw4_w8a8_linear_tokens", d, px, _TYPES[x.dtype], T, K, ldx, pw,
-          _flat(ws, "ws", _F32, d), N, ldw, py, _TYPES[out.dtype], ldy,
-          _flat(workspace, "workspace", _U8, d), ctypes.byref(ctypes.c_size_t(workspace.numel())))
+        workspace = x.new_empty(max(w8a8_workspace_bytes(T, K), 1), dtype=torch.uint8)
+    _call("dgw4_w8a8_linear_tokens", d, px, _TYPES[x.dtype], T, K, ldx, pw, pws, N, ldw, py,
+          _TYPES[out.dtype], ldy, _flat(workspace, "workspace", _U8, d),
+          ctypes.byref(ctypes.c_size_t(workspace.numel())))
     return out
