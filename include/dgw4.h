@@ -491,8 +491,9 @@ DGW4_API int dgw4_quantize_rows_i8(const void *x, int x_type, int rows, int K, l
  *       aligned to its element; elements between the rows are left as they are
  *   T >= 0, N >= 1 of any value; K >= 16, K % 16 == 0 (rows of
  *   dgw4_quantize_rows_i8 are zero-padded to that), K <= 131056 (the sum fits
- *   32 bits for all codes); ldx, ldw <= 2^22. DGW4_ERR_UNSUPPORTED where K or a
- *   row distance is out of these ranges, DGW4_ERR_INVALID_ARG for the rest.
+ *   32 bits for all codes); ldx, ldw <= 2^22; T, N < 2^31 - 256.
+ *   DGW4_ERR_UNSUPPORTED where one of these limits or K's multiple is not
+ *   kept, DGW4_ERR_INVALID_ARG for the rest.
  * T == 0 is a no-op. Enqueued on `stream`.
  */
 DGW4_API int dgw4_w8a8_linear(const int8_t *xq, const float *xs, int T, int K, long long ldx,

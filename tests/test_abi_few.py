@@ -116,7 +116,8 @@ def test_w8a8_rejects():
                dict(y=P + 1), dict(t=0, y=P + 2)):
         assert call(**kw) == B.ERR_INVALID_ARG, kw
     for kw in (dict(K=40, ldx=48, ldw=48), dict(K=131072, ldx=131072, ldw=131072),
-               dict(ldx=(1 << 22) + 16), dict(ldw=(1 << 22) + 16)):
+               dict(ldx=(1 << 22) + 16), dict(ldw=(1 << 22) + 16), dict(T=2**31 - 1),
+               dict(N=2**31 - 1, ldy=2**31)):
         assert call(**kw) == B.ERR_UNSUPPORTED, kw
     assert call(T=0, xq=None, xs=None, y=None) == B.OK
 

@@ -61,6 +61,22 @@ SHAPES = [
     dict(T=2, E=70, topk=64, d=128, m=64),             # the widest choice
     dict(T=5, E=6, topk=2, d=4096, m=1408, gg=64, dgr=128),
     dict(T=9, E=4, topk=2, d=640, m=64, gg=128, dgr=64, same_sign=True),
+    # past 64 assignments: every number of steps and scale pieces of down
+    dict(T=20, E=4, topk=4, d=256, m=704),
+    dict(T=17, E=5, topk=4, d=128, m=1024),
+    dict(T=33, E=3, topk=2, d=128, m=1408),
+    dict(T=70, E=2, topk=1, d=256, m=2048),
+    dict(T=23, E=6, topk=3, d=128, m=768, dgr=128),
+    dict(T=40, E=6, topk=2, d=384, m=1408, gg=64, dgr=128),
+    # up to 64: halves of m in one step and in several
+    dict(T=4, E=3, topk=2, d=128, m=1408),
+    dict(T=3, E=4, topk=4, d=256, m=2048),
+    dict(T=2, E=3, topk=1, d=128, m=64, dgr=64),
+    dict(T=1, E=3, topk=3, d=8192, m=128),             # the most groups of d
+    # routing inside the first launch: more than 128 experts, the widest choice
+    dict(T=7, E=200, topk=5, d=128, m=64),
+    dict(T=1, E=256, topk=64, d=128, m=64),
+    dict(T=64, E=129, topk=1, d=128, m=64),
 ]
 
 
@@ -78,6 +94,26 @@ def test_matches_plain_form(shape):
         assert few_ref.same_bits(out, again)
     routed = dg.moe_few_routed(c.x, c.logits, c.topk, gu, dn, workspace=ws)
     assert few_ref.same_bits(out, routed)
+
+
+@pytest.mark.parametrize("E", [5, 64, 65, 128, 130, 256])
+def test_routing_edges(E):
+    # ties to the lower id, +0 and -0 equal, negative values, subnormals and the
+    # extremes of fp32: the form from logits chooses and weighs as the router
+    T, topk = 8, min(E, 8)
+    c = Case(T=T, E=E, topk=topk, d=128, m=64, seed=11)
+    rng = np.random.default_rng(E)
+    lg = np.round(rng.standard_normal((T, E)) * 2).astype(np.float32)      # many ties
+    lg[1] = 0.5
+    lg[2] = np.where(np.arange(E) % 2 == 0, np.float32(0.0), np.float32(-0.0))
+    lg[3] = -np.abs(lg[3]) - 1
+    lg[4] = rng.choice(np.array([1e-40, -1e-40, 3.4e38, -3.4e38, 0], dtype=np.float32), E)
+    lg[5, :] = -3.4e38
+    lg[6] = rng.standard_normal(E) * 1e-3
+    logits = torch.from_numpy(lg).cuda()
+    ids, w = dg.router(logits, topk)
+    assert few_ref.same_bits(dg.moe_few_routed(c.x, logits, topk, c.gu, c.dn),
+                             dg.moe_few(c.x, ids, w, c.gu, c.dn))
 
 
 def test_agrees_with_the_layer():

@@ -668,7 +668,8 @@ int w8a8_sizes(int T, int Kp, int N, long long ldw, int y_type, long long ldy)
 {
     if (T < 0 || Kp < 1 || N < 1 || type_bytes(y_type) == 0 || ldw < Kp || ldw % 16 != 0 || ldy < N)
         return DGW4_ERR_INVALID_ARG;
-    return Kp > kMaxK8 || ldw > kMaxLd8 ? DGW4_ERR_UNSUPPORTED : DGW4_OK;
+    // T and N are rounded up to whole tiles in 32 bits
+    return Kp > kMaxK8 || ldw > kMaxLd8 || T > INT_MAX - 256 || N > INT_MAX - 256 ? DGW4_ERR_UNSUPPORTED : DGW4_OK;
 }
 
 }  // namespace

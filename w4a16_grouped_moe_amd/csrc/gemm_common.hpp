@@ -5,6 +5,8 @@
 
 #include "dgw4_internal.hpp"
 
+#include <atomic>
+
 namespace dgw4 {
 namespace {
 
@@ -200,6 +202,29 @@ hipError_t allow_lds(Kern kern, size_t lds, size_t &allowed)
         hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (err == hipSuccess)
         allowed = lds;
+    return err;
+}
+
+// The same for callers on any device: the allowance is each device's own.
+constexpr int kMaxDevices = 64;
+struct LdsAllowed {
+    std::atomic<size_t> bytes[kMaxDevices] = {};
+};
+
+template <class Kern>
+hipError_t allow_lds_here(Kern kern, size_t lds, LdsAllowed &allowed)
+{
+    if (lds <= 16 * 1024)
+        return hipSuccess;
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess)
+        return err;
+    if (dev < kMaxDevices && lds <= allowed.bytes[dev].load(std::memory_order_relaxed))
+        return hipSuccess;
+    err = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (err == hipSuccess && dev < kMaxDevices)
+        allowed.bytes[dev].store(lds, std::memory_order_relaxed);
     return err;
 }
 

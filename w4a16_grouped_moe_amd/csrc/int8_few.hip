@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
 template <int TB, class Ty>
 hipError_t run(I8FewArgs a, hipStream_t st)
 {
-    static size_t allowed = 24 * 1024;
+    static LdsAllowed allowed;
     const size_t lds = (size_t)a.g.T * code_stride(a.g.K);
-    const hipError_t err = allow_lds(i8_few_kernel<TB, Ty>, lds, allowed);
+    const hipError_t err = allow_lds_here(i8_few_kernel<TB, Ty>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int items = (a.g.N + 15) / 16;

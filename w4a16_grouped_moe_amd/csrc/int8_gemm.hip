@@ -136,9 +136,9 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
 template <int BN, int BT, int WN, int WT, int ST, class Ty>
 hipError_t run(const I8Args &a, hipStream_t st)
 {
-    static size_t allowed = 64 * 1024;
+    static LdsAllowed allowed;
     constexpr size_t lds = (size_t)ST * (BN + BT) * kStageK;
-    const hipError_t err = allow_lds(i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>, lds, allowed);
+    const hipError_t err = allow_lds_here(i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;

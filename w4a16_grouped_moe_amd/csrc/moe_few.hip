@@ -799,9 +799,9 @@ hipError_t run_gate_up(const FewArgs &a, bool routed, hipStream_t st)
 template <int G, bool TL, int NS>
 hipError_t run_down(const FewArgs &a, hipStream_t st)
 {
-    static size_t allowed = 24 * 1024;
+    static LdsAllowed allowed;
     const size_t lds = (size_t)a.A * (2 * (size_t)a.m + 16);
-    const hipError_t err = allow_lds(few_down_kernel<G, TL, NS>, lds, allowed);
+    const hipError_t err = allow_lds_here(few_down_kernel<G, TL, NS>, lds, allowed);
     if (err != hipSuccess)
         return err;
     few_down_kernel<G, TL, NS><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
@@ -811,9 +811,9 @@ hipError_t run_down(const FewArgs &a, hipStream_t st)
 template <int G, bool TL, int NS, bool MULTI>
 hipError_t run_down_items(const FewArgs &a, hipStream_t st)
 {
-    static size_t allowed = 32 * 1024;
+    static LdsAllowed allowed;
     const size_t lds = 16 * (2 * (size_t)a.m + 16);
-    hipError_t err = allow_lds(few_down_items_kernel<G, TL, NS, MULTI>, lds, allowed);
+    hipError_t err = allow_lds_here(few_down_items_kernel<G, TL, NS, MULTI>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int items = a.A * (a.d / 16);
