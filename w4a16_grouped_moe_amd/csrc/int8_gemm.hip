@@ -14,6 +14,15 @@
 // v_mfma_i32_16x16x64_i8 takes the channels as its row operand: a lane ends
 // with four consecutive channels of one token. The sums are exact, so their
 // order is of no matter.
+//
+// The 256 x 256 tile reaches 1.9 POP/s at T = 4096, K = 2816, N = 11264 (132 us;
+// 704 tiles are 2.75 rounds of the chip) and 2.2 to 2.37 at K = 8192 (T = 2048, N
+// = 8192). Registers-only MFMA chains on such codes run at 3.2 to 3.4 POP/s on
+// the same card and 4.5 on zeros, the clock falling to 1.9 to 2.2 GHz in the
+// products: the power the chip may draw bounds them, and deeper pipelines (four
+// stages of 64 bytes), fragments held a half stage ahead, waves that only copy
+// (with the tiles of a run overlapping their stores) and smaller tiles two to
+// a CU all measured the same or slower.
 #include "int8_common.hpp"
 
 #include <cmath>
@@ -115,20 +124,24 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
     }
     stage_barrier<0>();                  // no copy may still land when the workgroup ends
 
+    // every scale before the first store: a load behind stores waits for them
     const bool vec = rows_in_fours<Ty>(a);
     f32x4 ws[NA];
+    float xs[NB];
 #pragma unroll
     for (int i = 0; i < NA; ++i)
         ws[i] = channel_scales(a, n0 + wn + i * 16 + 4 * p);
 #pragma unroll
+    for (int j = 0; j < NB; ++j)
+        xs[j] = a.xs[min(t0 + wt + j * 16 + r, a.T - 1)];
+#pragma unroll
     for (int j = 0; j < NB; ++j) {
         const int t = t0 + wt + j * 16 + r;
         if (t < a.T) {
-            const float xs = a.xs[t];
             Ty *y = (Ty *)a.y + (size_t)t * a.ldy;
 #pragma unroll
             for (int i = 0; i < NA; ++i)
-                store4<Ty>(y, n0 + wn + i * 16 + 4 * p, a.N, vec, acc[i][j], xs, ws[i]);
+                store4<Ty>(y, n0 + wn + i * 16 + 4 * p, a.N, vec, acc[i][j], xs[j], ws[i]);
         }
     }
 }
@@ -168,7 +181,10 @@ hipError_t pick(const I8Args &a, hipStream_t st)
         if (est[i] < est[best])
             best = i;
     switch (best) {
-    case 0: return run<256, 256, 64, 128, 2, Ty>(a, st);
+    // one tile of tokens: waves of 128 channels x 64 tokens store longer rows
+    // (T = 256, N = 262144, fp32: 244 us against 254); else 64 x 128 is level or
+    // 1 to 2% faster
+    case 0: return a.T <= 256 ? run<256, 256, 128, 64, 2, Ty>(a, st) : run<256, 256, 64, 128, 2, Ty>(a, st);
     case 1: return run<256, 128, 64, 64, 3, Ty>(a, st);
     case 2: return run<128, 128, 64, 32, 4, Ty>(a, st);
     case 3: return run<64, 64, 32, 32, 4, Ty>(a, st);
