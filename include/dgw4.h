@@ -410,19 +410,23 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
                                  void *stream);
 
 /*
- * dgw4_moe_few — the routed-expert layer of dgw4_moe_forward for few tokens,
- * in two launches: at most 512 assignments (T * topk; 64 tokens at top-8).
- * Each launch splits the chosen experts' weights over the whole chip, where
- * dgw4_moe_forward gives half an expert to one workgroup: the form for one
- * token to a few dozen. The formula, the packed weights in either layout and
- * the treatment of ids (outside [0, E): no contribution; equal ids: each
- * counts) are dgw4_moe_forward's. Sums are fp32, each group's scale applied
- * to an fp32 partial sum of exact integers times x; the gated intermediate is
- * rounded to fp16 once, the expert outputs stay in fp32 until they are
- * weighted and added in ascending k, and out is rounded to fp16 once. The
- * results agree with dgw4_moe_forward's up to rounding and repeated calls
- * give identical bits. A row of x that no live id names is not read into any
- * other row's result; a token without live ids gets zeros.
+ * dgw4_moe_few — the routed-expert layer of dgw4_moe_forward for few tokens:
+ * at most 512 assignments (T * topk; 64 tokens at top-8). Two launches up to 64
+ * assignments (gate_up with its activation; down with the weighted sum), three
+ * beyond (the sum apart). Each launch splits the chosen experts' weights over
+ * the whole chip, where dgw4_moe_forward gives half an expert to one
+ * workgroup: the form for one token to a few dozen (at 128 experts, top-8, d =
+ * 2816, m = 704 it is the faster one up to about 24 tokens; past that the two
+ * are within a few per cent).
+ * The formula, the packed weights in either layout and the treatment of ids
+ * (outside [0, E): no contribution; equal ids: each counts) are
+ * dgw4_moe_forward's. Sums are fp32, each group's scale applied to an fp32
+ * partial sum of exact integers times x; the gated intermediate is rounded to
+ * fp16 once, the expert outputs stay in fp32 until they are weighted and added
+ * in ascending k, and out is rounded to fp16 once. The results agree with
+ * dgw4_moe_forward's up to rounding and repeated calls give identical bits. A
+ * row of x enters its own token's results only; a token without live ids gets
+ * zeros.
  *   T >= 0, 1 <= topk <= E, 1 <= E <= 1024, d % gu_g == 0, m % dn_g == 0;
  *   gu_g, dn_g: 64 or 128, each or-ed with DGW4_WEIGHTS_TILED where that
  *   stack is tiled; the DGW4_ROWS_* bits are refused (INVALID_ARG).
@@ -442,8 +446,9 @@ DGW4_API int dgw4_moe_few(const uint16_t *x, const int32_t *topk_ids, const floa
 /*
  * dgw4_moe_few_routed — dgw4_moe_few from router logits (device fp32 [T, E],
  * finite, 4-byte aligned; topk <= 64): the same ids and weights as
- * dgw4_router's, then the layer. The same workspace size and the same bits as
- * dgw4_router followed by dgw4_moe_few.
+ * dgw4_router's, then the layer. Up to 8 tokens and 256 experts the first
+ * launch routes them itself; else dgw4_router's launch goes first. The same
+ * workspace size and the same bits as dgw4_router followed by dgw4_moe_few.
  */
 DGW4_API int dgw4_moe_few_routed(const uint16_t *x, const float *router_logits, int T, int topk,
                                  int E, int d, int m, const uint8_t *gu_q, const uint16_t *gu_s,
