@@ -111,6 +111,22 @@ def test_product(T, K, N, dtype):
     assert few_ref.same_bits(y, few_ref.product(xq, xs, wq, ws, dtype))
 
 
+# each tile of the product, K in whole turns of its parts and not (the last
+# parts' stages past K), channels and tokens that end inside a tile
+@pytest.mark.parametrize("T,K,N", [(770, 16, 11565), (646, 144, 13129), (200, 144, 40001), (657, 16, 9631),
+                                   (587, 144, 9625), (835, 16, 4549), (322, 144, 10061), (194, 704, 8146),
+                                   (200, 832, 7998), (250, 2800, 4001), (36, 16, 8293), (33, 144, 9906),
+                                   (35, 48, 4868), (35, 176, 5205), (59, 112, 35), (77, 4112, 81),
+                                   (40, 8208, 35), (65, 6000, 100)])
+def test_product_tiles(T, K, N):
+    rng = np.random.default_rng([T, K, N])
+    (xq, xs), (wq, ws) = _codes(rng, T, K), _codes(rng, N, K)
+    xd, sd, wd, vd = _dev(xq, xs, wq, ws)
+    for dtype in TYPES:
+        y = dg.w8a8_linear(xd, sd, (wd, vd), dtype=dtype)
+        assert few_ref.same_bits(y, few_ref.product(xq, xs, wq, ws, dtype))
+
+
 @pytest.mark.parametrize("T", [1, 9, 70, 300])
 def test_product_extremes(T):
     # the largest sums (all codes -128 at the longest K), zeros, and scales

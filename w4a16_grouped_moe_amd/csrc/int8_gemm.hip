@@ -2,7 +2,9 @@
 // in LDS tiles.
 //
 // A workgroup takes BN channels x BT tokens and walks K in stages of 128
-// bytes, ST stages deep in LDS. A stage's rows (BN of W, then BT of X, 128
+// bytes, ST stages deep in LDS; with few tiles KS groups of its waves take every
+// KS-th stage each and add their sums through LDS (a stage costs a barrier and
+// the LDS's latency whatever its size). A stage's rows (BN of W, then BT of X, 128
 // bytes each, whole cache lines) are copied from global memory straight into
 // LDS, 16 bytes a lane, without passing through registers; one barrier per
 // stage. Position c of a row's eight 16-byte pieces holds piece c ^ (row % 8),
@@ -32,8 +34,8 @@ namespace {
 
 constexpr int kStageK = 128;                     // bytes of K per stage
 
-template <int BN, int BT, int WN, int WT, int ST, class Ty>
-__global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8Args a, int tiles_n, int tiles_t)
+template <int BN, int BT, int WN, int WT, int ST, int KS, class Ty>
+__global__ void __launch_bounds__(KS *(BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8Args a, int tiles_n, int tiles_t)
 {
     constexpr int kWaves = (BN / WN) * (BT / WT);
     constexpr int kLoadsW = BN / 8 / kWaves, kLoadsX = BT / 8 / kWaves;   // copies per wave and stage, 8 rows each
@@ -43,7 +45,8 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
     static_assert(BN % (8 * kWaves) == 0 && BT % (8 * kWaves) == 0, "whole copies for each wave");
     extern __shared__ char s_mem[];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wave_id = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wave = wave_id % kWaves, part = wave_id / kWaves;           // part: its stages are part, part + KS, ...
     const int r = lane & 15, p = lane >> 4;
 
     // workgroup -> tile: an XCD (workgroups i, i + 8, ...) takes a contiguous run
@@ -69,13 +72,14 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
         off[i] = i < kLoadsW
                      ? (uint32_t)min((wave * kLoadsW + i) * 8 + (lane >> 3), rows_w - 1) * (uint32_t)a.ldw + kl
                      : (uint32_t)min((wave * kLoadsX + i - kLoadsW) * 8 + (lane >> 3), rows_x - 1) * (uint32_t)a.ldx + kl;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)s_mem;
+    char *const s_part = s_mem + part * (ST * kStage);
+    const uint32_t lds0 = lds_offset(s_part);
     const uint32_t lds_w = lds0 + (uint32_t)(wave * kLoadsW * 1024);
     const uint32_t lds_x = lds0 + (uint32_t)(BN * kStageK + wave * kLoadsX * 1024);
 
-    const int stages = (a.K + kStageK - 1) / kStageK;
+    const int stages = (a.K + KS * kStageK - 1) / (KS * kStageK);         // of each part; past K they read zeros
     auto issue = [&](int st, int buf) {
-        const uint32_t k0 = (uint32_t)st * kStageK;
+        const uint32_t k0 = (uint32_t)(st * KS + part) * kStageK;
         const bool in_k = k0 + kl < (uint32_t)a.K;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
@@ -105,8 +109,8 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
         for (int kk = 0; kk < 2; ++kk) {
             i32x4 fw[NA], fx[NB];
             // piece 4 kk + p of the row: the two halves' positions differ in bit 2
-            const char *ra = s_mem + ((fa + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
-            const char *rb = s_mem + ((fb + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
+            const char *ra = s_part + ((fa + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
+            const char *rb = s_part + ((fb + (uint32_t)(buf * kStage)) ^ (uint32_t)(kk * 64));
 #pragma unroll
             for (int i = 0; i < NA; ++i)
                 fw[i] = *reinterpret_cast<const i32x4 *>(ra + i * 16 * kStageK);
@@ -123,6 +127,25 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
         nbuf = nbuf + 1 == ST ? 0 : nbuf + 1;
     }
     stage_barrier<0>();                  // no copy may still land when the workgroup ends
+
+    // the parts' sums, over the stages that no wave reads any more
+    if constexpr (KS > 1) {
+        static_assert((KS - 1) * kWaves * NA * NB * 1024 <= KS * ST * kStage, "the sums fit the stages");
+        auto *s_sum = reinterpret_cast<i32x4 *>(s_mem);
+        if (part > 0) {
+#pragma unroll
+            for (int i = 0; i < NA * NB; ++i)
+                s_sum[(((part - 1) * kWaves + wave) * NA * NB + i) * 64 + lane] = acc[i / NB][i % NB];
+        }
+        __syncthreads();
+        if (part > 0)
+            return;
+#pragma unroll
+        for (int q = 0; q < KS - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < NA * NB; ++i)
+                acc[i / NB][i % NB] += s_sum[((q * kWaves + wave) * NA * NB + i) * 64 + lane];
+    }
 
     // every scale before the first store: a load behind stores waits for them
     const bool vec = rows_in_fours<Ty>(a);
@@ -146,49 +169,75 @@ __global__ void __launch_bounds__((BN / WN) * (BT / WT) * 64) i8_gemm_kernel(I8A
     }
 }
 
-template <int BN, int BT, int WN, int WT, int ST, class Ty>
+template <int BN, int BT, int WN, int WT, int ST, int KS, class Ty>
 hipError_t run(const I8Args &a, hipStream_t st)
 {
     static LdsAllowed allowed;
-    constexpr size_t lds = (size_t)ST * (BN + BT) * kStageK;
-    const hipError_t err = allow_lds_here(i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>, lds, allowed);
+    constexpr size_t lds = (size_t)KS * ST * (BN + BT) * kStageK;
+    const hipError_t err = allow_lds_here(i8_gemm_kernel<BN, BT, WN, WT, ST, KS, Ty>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
-    i8_gemm_kernel<BN, BT, WN, WT, ST, Ty>
-        <<<dim3(tn * tt), dim3((BN / WN) * (BT / WT) * 64), lds, st>>>(a, tn, tt);
+    i8_gemm_kernel<BN, BT, WN, WT, ST, KS, Ty>
+        <<<dim3(tn * tt), dim3(KS * (BN / WN) * (BT / WT) * 64), lds, st>>>(a, tn, tt);
     return hipGetLastError();
 }
 
-// The tile by the least estimated time: rounds of workgroups over the chip
-// times a round's time, measured at K = 2816 (22 stages; all scale with K).
-// 256 x 256 and 256 x 128 tiles fill a CU alone; the small ones share it and
-// are then bound by their rate (us per tile and CU) rather than a round.
-//   256 x 256: 42 us a round    256 x 128: 27    128 x 128: 17
-//   64 x 64: 9.0, or 6.5 per tile and CU    64 x 32: 7.5, or 4.1
-// At T = 512, N = 2816: 40.2 / 24.8 / 16.5 / 12.1 / 13.3 us measured; at T = 512,
-// N = 32768: 52.2 / 59.7 / 77.8 / 104 / 130.
+// The tile by the least estimated time, in us past what every launch costs: a
+// workgroup takes fixed + stage * (128-byte stages of K), times the rounds of
+// the chip's 256 compute units. A workgroup that fills one by its LDS runs in
+// whole rounds (per_cu 0); the others share it, per_cu of them in a workgroup's
+// time. Fitted to 68 shapes (33 to 4096 tokens, 64 to 65536 channels, K 704 to
+// 16384) that every tile was timed on: the choice is within 1% of the best
+// tile on average and 11% at worst, where tiles of whole K alone were 20% and
+// 117% off. Some, us, 64 x 32 with whole K / the tile taken now:
+//   T 252, N 737, K 8544: 17.1 / 10.5 (32 x 32, four parts of K)
+//   T 256, N 4096, K 2816: 9.8 / 8.4 (64 x 64, two parts)
+//   T 128, N 4096, K 4096: 10.0 / 8.3 (64 x 32, two parts)
+struct I8Tile {
+    int bn, bt;
+    double stage, fixed, per_cu;
+};
+constexpr I8Tile kTiles[] = {
+    {256, 256, 1.80, 8.1, 0.0}, {256, 128, 0.94, 6.1, 0.0}, {128, 128, 0.59, 3.7, 0.0},
+    {64, 128, 0.34, 2.8, 0.0},  {64, 64, 0.24, 1.7, 0.0},   {64, 64, 0.30, 0.9, 1.1},
+    {64, 32, 0.15, 0.8, 0.8},   {32, 32, 0.11, 0.7, 1.0},   {32, 32, 0.093, 1.6, 0.0},
+};
+
+int pick_tile(const I8Args &a)
+{
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    int best = 0;
+    double least = HUGE_VAL;
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        const I8Tile &t = kTiles[i];
+        const double tiles = (double)((a.N + t.bn - 1) / t.bn) * ((a.T + t.bt - 1) / t.bt) / 256.0;
+        const double rounds = t.per_cu == 0.0 ? ceil(tiles) : fmax(1.0, tiles / t.per_cu);
+        const double us = (t.fixed + t.stage * stages) * rounds;
+        if (us < least) {
+            least = us;
+            best = i;
+        }
+    }
+    return best;
+}
+
 template <class Ty>
 hipError_t pick(const I8Args &a, hipStream_t st)
 {
-    auto tiles = [&](int bn, int bt) {
-        return (double)((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt) / 256.0;
-    };
-    const double est[5] = {42.0 * ceil(tiles(256, 256)), 27.0 * ceil(tiles(256, 128)), 17.0 * ceil(tiles(128, 128)),
-                           fmax(9.0, 6.5 * tiles(64, 64)), fmax(7.5, 4.1 * tiles(64, 32))};
-    int best = 0;
-    for (int i = 1; i < 5; ++i)
-        if (est[i] < est[best])
-            best = i;
-    switch (best) {
+    switch (pick_tile(a)) {
     // one tile of tokens: waves of 128 channels x 64 tokens store longer rows
     // (T = 256, N = 262144, fp32: 244 us against 254); else 64 x 128 is level or
     // 1 to 2% faster
-    case 0: return a.T <= 256 ? run<256, 256, 128, 64, 2, Ty>(a, st) : run<256, 256, 64, 128, 2, Ty>(a, st);
-    case 1: return run<256, 128, 64, 64, 3, Ty>(a, st);
-    case 2: return run<128, 128, 64, 32, 4, Ty>(a, st);
-    case 3: return run<64, 64, 32, 32, 4, Ty>(a, st);
-    default: return run<64, 32, 32, 16, 4, Ty>(a, st);
+    case 0: return a.T <= 256 ? run<256, 256, 128, 64, 2, 1, Ty>(a, st) : run<256, 256, 64, 128, 2, 1, Ty>(a, st);
+    case 1: return run<256, 128, 64, 64, 3, 1, Ty>(a, st);
+    case 2: return run<128, 128, 64, 32, 4, 1, Ty>(a, st);
+    case 3: return run<64, 128, 32, 64, 3, 2, Ty>(a, st);
+    case 4: return run<64, 64, 32, 32, 3, 2, Ty>(a, st);
+    case 5: return run<64, 64, 32, 32, 2, 2, Ty>(a, st);
+    case 6: return run<64, 32, 32, 16, 3, 2, Ty>(a, st);
+    case 7: return run<32, 32, 16, 16, 4, 2, Ty>(a, st);
+    default: return run<32, 32, 16, 16, 4, 4, Ty>(a, st);
     }
 }
 
