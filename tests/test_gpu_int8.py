@@ -49,6 +49,27 @@ def test_quantize_rows(rows, K, dtype):
     assert np.array_equal(s.cpu().numpy().view(np.int32), rs.view(np.int32))
 
 
+# both sides of each length at which another number of threads takes a row, and
+# every length of a last vector
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,K", [(70, K) for K in (1, 2, 7, 8, 9, 10, 11, 12, 13, 14, 15, 127, 128, 129, 383, 384,
+                                                      385, 767, 768, 769, 1023, 1024, 1025, 1535, 1536, 1537, 2999,
+                                                      4095, 4096, 4097, 8191, 8192, 8193, 16383, 16385)] +
+                         [(8191, 1601), (8200, 1601), (8195, 2998)])
+def test_quantize_lengths(rows, K, dtype):
+    rng = np.random.default_rng([rows, K, 1])
+    x = _acts(rng, rows, K, dtype)
+    x[-1] = 0
+    x[-1, K - 1] = -0.25                  # the row's maximum in its last column
+    if rows >= 70:
+        x[3, K // 2] = float("nan")
+        x[5, K - 1] = float("inf")
+    q, s = dg.quantize_rows_i8(x.cuda())
+    rq, rs = few_ref.quantize_rows(x)
+    assert np.array_equal(q.cpu().numpy(), rq)
+    assert np.array_equal(s.cpu().numpy(), rs, equal_nan=True)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_quantize_edges(dtype):
     # zeros, one sign, ties of the rounding, the type's extremes and subnormals,

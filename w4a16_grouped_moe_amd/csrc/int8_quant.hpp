@@ -1,4 +1,4 @@
-// One row's symmetric 8-bit quantisation by one wave (not part of the ABI).
+// Symmetric 8-bit quantisation of rows (not part of the ABI).
 //
 //   s = max|x| / 127 (1 if that is zero), q = clamp(rint(x / s), -127, 127),
 // each operation rounded to fp32; a row with a NaN or an infinity: s = NaN,
@@ -22,18 +22,51 @@ struct Vec8 {
     typedef Tx type __attribute__((ext_vector_type(8)));
 };
 
-// Eight values of a row from k on (0 past K), whole vectors at any alignment
-// of the element.
+// v moved down by d elements (0 < d < 8), zeros above.
+template <class V>
+__device__ inline V moved_down(V v, int d)
+{
+    constexpr int kDwords = sizeof(V) / 4;
+    typedef uint32_t dwords __attribute__((ext_vector_type(kDwords)));
+    dwords u = __builtin_bit_cast(dwords, v);
+    auto by = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < kDwords; ++i)
+            u[i] = i + n < kDwords ? u[(i + n) % kDwords] : 0u;
+    };
+    if (d & 4)
+        by(kDwords / 2);
+    if (d & 2)
+        by(kDwords / 4);
+    if (d & 1) {
+        if constexpr (kDwords == 8) {
+            by(1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kDwords; ++i)
+                u[i] = u[i] >> 16 | (i + 1 < kDwords ? u[(i + 1) % kDwords] << 16 : 0u);
+        }
+    }
+    return __builtin_bit_cast(V, u);
+}
+
+// Eight values of a row from k on (0 past K), at any alignment of the element.
+// Past K - 8 the row's last eight are loaded and moved, so that no load waits
+// for a branch.
 template <class Tx>
 __device__ inline typename Vec8<Tx>::type load8(const Tx *row, int k, int K)
 {
-    typename Vec8<Tx>::type v;
-    if (k + 8 <= K) {
-        __builtin_memcpy(&v, row + k, sizeof v);
+    typename Vec8<Tx>::type v{};
+    if (K >= 8) {
+        const int at = min(k, K - 8);
+        __builtin_memcpy(&v, row + at, sizeof v);
+        if (at < k)
+            v = k >= K ? typename Vec8<Tx>::type{} : moved_down(v, k - at);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = k + i < K ? row[k + i] : (Tx)0.0f;
+        for (int i = 0; i < 7; ++i)
+            if (k + i < K)
+                v[i] = row[k + i];
     }
     return v;
 }
@@ -125,16 +158,18 @@ __device__ inline uint2 codes8(typename Vec8<Tx>::type v, const RowScale &rs)
     return rs.finite ? o : make_uint2(0, 0);
 }
 
-__device__ inline uint32_t wave_top(uint32_t v)
+// The maximum over N neighbouring lanes.
+template <int N>
+__device__ inline uint32_t lanes_top(uint32_t v)
 {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
+    for (int o = N / 2; o > 0; o >>= 1)
         v = max(v, (uint32_t)__shfl_xor((int)v, o));
     return v;
 }
 
-// Vector i (eight values) of a row by threads tid of N (a wave, or a workgroup
-// with room for its waves' maxima in s_part): the row's codes into q[0 .. end)
+// A row by threads tid of N (neighbouring lanes of a wave, or a workgroup with
+// room for its waves' maxima in s_part), eight values at a time: the row's codes into q[0 .. end)
 // (8-byte aligned, end a multiple of 16, zero from K on); returns the scale in
 // every thread. The first kKept vectors of a thread stay in registers between
 // the maximum and the codes.
@@ -151,7 +186,7 @@ __device__ inline float quantize_row(const Tx *__restrict__ row, int K, int end,
         top = max(top, top8(v[j]));
     for (int k = (kKept * N + tid) * 8; k < K; k += N * 8)
         top = max(top, top8(load8<Tx>(row, k, K)));
-    top = wave_top(top);
+    top = lanes_top<(N < 64 ? N : 64)>(top);
     if constexpr (N > 64) {
         if ((tid & 63) == 0)
             s_part[tid >> 6] = top;
