@@ -724,8 +724,6 @@ int dgw4_w8a8_linear(const int8_t *xq, const float *xs, int T, int K, long long 
         !aligned(xs, 4) || !aligned(ws, 4) || !aligned(y, type_bytes(y_type)))
         return DGW4_ERR_INVALID_ARG;
     const dgw4::I8Args a{xq, xs, wq, ws, T, K, N, ldx, ldw, ldy, y, y_type};
-    if (dgw4::i8_few_fits(T, K))
-        return from_hip(dgw4::launch_i8_few({a, nullptr, dgw4::kI8Codes, K, 0, 0, 0}, (hipStream_t)stream));
     return from_hip(dgw4::launch_w8a8_linear(a, (hipStream_t)stream));
 }
 
@@ -759,14 +757,12 @@ int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, long long l
     int8_t *xq = static_cast<int8_t *>(workspace);
     float *xs = reinterpret_cast<float *>(static_cast<char *>(workspace) + q_bytes);
     const dgw4::I8Args a{xq, xs, wq, ws, T, Kp, N, Kp, ldw, ldy, y, y_type};
-    if (T <= dgw4::kI8FewQuantised && dgw4::i8_few_fits(T, Kp))
-        return from_hip(dgw4::launch_i8_few({a, x, x_type, K, ldx, 0, 0}, (hipStream_t)stream));
+    if (T <= dgw4::kI8FewTokens && (long long)T * Kp <= dgw4::kI8FewCodes)
+        return from_hip(dgw4::launch_i8_few({a, x, x_type, K, ldx, 0}, (hipStream_t)stream));
     const hipError_t err =
         dgw4::launch_quantize_rows(x, x_type, T, K, ldx, xq, Kp, xs, (hipStream_t)stream);
     if (err != hipSuccess)
         return from_hip(err);
-    if (dgw4::i8_few_fits(T, Kp))
-        return from_hip(dgw4::launch_i8_few({a, nullptr, dgw4::kI8Codes, Kp, 0, 0, 0}, (hipStream_t)stream));
     return from_hip(dgw4::launch_w8a8_linear(a, (hipStream_t)stream));
 }
 

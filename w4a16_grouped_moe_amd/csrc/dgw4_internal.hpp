@@ -191,25 +191,23 @@ struct I8Args {
 
 hipError_t launch_w8a8_linear(const I8Args &a, hipStream_t stream);
 
-// The product for few tokens (int8_few.hip): up to kI8FewTokens whose codes fit
-// LDS, from codes (x_type kI8Codes) or from activations x of x_type [T, k_x],
-// rows ld apart (g.xq and g.xs unused, g.K = k_x in whole 16s).
-constexpr int kI8FewTokens = 32;
-// Tokens quantised inside the product's launch: every workgroup does all of
-// them (about 0.6 us a token at K = 2816), a launch before it costs 3.6 us.
-constexpr int kI8FewQuantised = 6;
-constexpr int kI8Codes = -1;
+// The product straight from a few tokens' activations x of x_type [T, k_x], rows
+// ld apart (int8_few.hip; g.xq and g.xs unused, g.K = k_x in whole 16s): up to
+// kI8FewTokens tokens of kI8FewCodes values in all. Every workgroup quantises
+// all of them, about 0.6 us for 2816 values, where a launch before the product
+// costs 3 us: 6 tokens of 2816 to 2048 channels 7.9 us against 8.7 in two
+// launches, 1 of 16384 14.2 against 17.3, but 4 of 8192 13.6 against 11.4.
+constexpr int kI8FewTokens = 6;
+constexpr int kI8FewCodes = 18 * 1024;
 
 struct I8FewArgs {
     I8Args g;
     const void *x;
     int x_type, k_x;
     long long ld;
-    uint32_t row_magic;         // set by launch_i8_few, as is run
-    int run;                    // neighbouring blocks of 16 channels a workgroup takes in turn
+    uint32_t row_magic;         // set by launch_i8_few
 };
 
-bool i8_few_fits(int T, int K);
 hipError_t launch_i8_few(I8FewArgs a, hipStream_t stream);
 
 // y: `halves` (1 or 2) fp16 arrays [T * topk, d] one after the other; each

@@ -39,31 +39,25 @@ __device__ inline Ty scaled(int acc, float xs, float ws)
     return from_f32<Ty>(__fmul_rn(__fmul_rn((float)acc, xs), ws));
 }
 
-// Four neighbouring outputs of a row, channels c .. c + 3 of N: one store where
-// the row allows it (vec: y and ldy in whole fours), element stores else.
+// Four neighbouring outputs of a row, channels c .. c + 3 of N, at any alignment
+// of the element: one store (rows of odd length stay near the rate of aligned
+// ones), element stores where the row ends.
 template <class Ty>
-__device__ inline void store4(Ty *row, int c, int N, bool vec, i32x4 acc, float xs, f32x4 ws)
+__device__ inline void store4(Ty *row, int c, int N, i32x4 acc, float xs, f32x4 ws)
 {
     typedef Ty ty4 __attribute__((ext_vector_type(4)));
-    if (vec && c + 3 < N) {
-        ty4 v;
+    ty4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = scaled<Ty>(acc[i], xs, ws[i]);
-        *reinterpret_cast<ty4 *>(row + c) = v;
+    for (int i = 0; i < 4; ++i)
+        v[i] = scaled<Ty>(acc[i], xs, ws[i]);
+    if (c + 3 < N) {
+        __builtin_memcpy(row + c, &v, sizeof v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 3; ++i)
             if (c + i < N)
-                row[c + i] = scaled<Ty>(acc[i], xs, ws[i]);
+                row[c + i] = v[i];
     }
-}
-
-// Whether rows of y may be stored four elements at a time.
-template <class Ty>
-__device__ inline bool rows_in_fours(const I8Args &a)
-{
-    return a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(Ty))) == 0;
 }
 
 // The scales of channels c .. c + 3 (0 past N).

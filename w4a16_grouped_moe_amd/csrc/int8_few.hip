@@ -1,21 +1,23 @@
-// Products of 8-bit rows for few tokens (up to 32), y[t, n] = xs[t] ws[n]
-// sum_k xq wq, from codes or straight from activations.
+// The product straight from a few tokens' activations (up to 6), y[t, n] = xs[t]
+// ws[n] sum_k xq wq, xs and xq quantised on the way.
 //
-// The weights, read once, are all the work. The tokens' codes lie in LDS
-// (quantised there from the activations, or copied), rows 16 bytes off the
-// bank period so that the 16 rows of an MFMA fragment fall on all banks, zero
-// past K. A workgroup takes 16 channels at a time, its eight waves every
-// eighth 128 bytes of K each; a wave holds six fragments of weights (16
-// channels x 64 bytes) and refills each with the next step's as soon as it has
-// been used. v_mfma_i32_16x16x64_i8 takes the channels as its row operand; the
-// waves' sums meet in LDS (integers: their order is of no matter).
+// The weights, read once, are all the work. Every workgroup quantises the
+// tokens into LDS, rows 16 bytes off the bank period so that the 16 rows of an
+// MFMA fragment fall on all banks, zero past K. It takes 16 channels at a time,
+// its eight waves every eighth 128 bytes of K each; a wave holds six fragments
+// of weights (16 channels x 64 bytes) and refills each with the next step's as
+// soon as it has been used. v_mfma_i32_16x16x64_i8 takes the channels as its row
+// operand; the waves' sums meet in LDS (integers: their order is of no matter).
 //
 // The workgroups running at one time read neighbouring rows (turn i goes to
 // workgroup i % grid). At 262144 channels of K = 2816 one token takes 126 us,
-// 5.9 TB/s of weights, five from fp32 134 us; giving each workgroup one
-// contiguous run of channels took 133 us, more loads in flight (8 or 12
-// fragments a wave) or copies into LDS in whole lines changed nothing, and
-// non-temporal loads cost 12 us.
+// 5.9 TB/s of weights, five 135; giving each workgroup one contiguous run of
+// channels took 133 us, more loads in flight (8 or 12 fragments a wave) or
+// copies into LDS in whole lines changed nothing, and non-temporal loads cost
+// 12 us. Codes at hand go through the tiles (int8_gemm.hip): from 9 tokens, or
+// with short rows, those are as fast or faster (25 tokens, 32768 channels, K
+// 1024: 8.7 us against 12.1 here), with fewer and K = 2816 within half a
+// microsecond.
 #include "int8_common.hpp"
 #include "int8_quant.hpp"
 
@@ -43,7 +45,7 @@ __device__ inline void codes_from(const I8FewArgs &a, char *codes, float *s_xs, 
         s_top[threadIdx.x] = 0u;
     __syncthreads();
     typename Vec8<Tx>::type v[kKeep];
-    // i / pieces, exact for i * pieces < 2^32: i < total <= 15360 here
+    // i / pieces, exact for i * pieces < 2^32: i < total <= 2400 here
     auto row_of = [&](int i) { return (int)__umulhi((uint32_t)i, a.row_magic); };
     auto load = [&](int i) {
         const int t = row_of(i), k = (i - t * pieces) * 8;
@@ -92,27 +94,13 @@ __device__ inline void codes_from(const I8FewArgs &a, char *codes, float *s_xs, 
         emit(load(i), i);
 }
 
-__device__ inline void codes_copied(const I8FewArgs &a, char *codes, float *s_xs)
-{
-    const int stride = code_stride(a.g.K), pieces = stride / 16 - 1;
-    for (int i = threadIdx.x; i < a.g.T * pieces; i += kI8Threads) {
-        const int t = i / pieces, c = i - t * pieces;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c * 16 < a.g.K)
-            v = *reinterpret_cast<const uint4 *>(a.g.xq + (size_t)t * a.g.ldx + c * 16);
-        *reinterpret_cast<uint4 *>(codes + t * stride + c * 16) = v;
-    }
-    if ((int)threadIdx.x < a.g.T)
-        s_xs[threadIdx.x] = a.g.xs[threadIdx.x];
-}
-
-template <int TB, class Ty>
+template <class Ty>
 __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
 {
-    __shared__ float s_xs[16 * TB];
-    __shared__ uint32_t s_top[16 * TB];
-    __shared__ RowScale s_rs[16 * TB];
-    __shared__ i32x4 s_red[2][kI8Waves][TB][64];
+    __shared__ float s_xs[kI8FewTokens];
+    __shared__ uint32_t s_top[kI8FewTokens];
+    __shared__ RowScale s_rs[kI8FewTokens];
+    __shared__ i32x4 s_red[2][kI8Waves][64];
     extern __shared__ __attribute__((aligned(16))) char s_codes[];    // [T][code_stride(K)]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -122,7 +110,7 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
     const int items = (a.g.N + 15) / 16;                   // of 16 channels
     const int mine = (units - wave + kI8Waves - 1) / kI8Waves;    // this wave's units: wave, wave + 8, ... (maybe none)
     const int batches = (units + kI8Waves * kHeld - 1) / (kI8Waves * kHeld);
-    int it = (int)blockIdx.x * a.run;
+    int it = (int)blockIdx.x;
 
     struct Source {
         rsrc_t rsrc;
@@ -160,54 +148,43 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
     switch (a.x_type) {
     case DGW4_F32: codes_from<float>(a, s_codes, s_xs, s_top, s_rs); break;
     case DGW4_F16: codes_from<_Float16>(a, s_codes, s_xs, s_top, s_rs); break;
-    case DGW4_BF16: codes_from<__bf16>(a, s_codes, s_xs, s_top, s_rs); break;
-    default: codes_copied(a, s_codes, s_xs);
+    default: codes_from<__bf16>(a, s_codes, s_xs, s_top, s_rs);
     }
     __syncthreads();
-    const char *xp[TB];
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
-        xp[tb] = s_codes + min(tb * 16 + r, a.g.T - 1) * stride + p * 16;
+    const char *xp = s_codes + min(r, a.g.T - 1) * stride + p * 16;
     int buf = 0;
-    i32x4 acc[TB];
+    i32x4 acc;
     for (int b = 0; it < items;) {
         const bool last = b == batches - 1;
-        const int nit = !last ? it : (it + 1) % a.run ? it + 1 : it + 1 + ((int)gridDim.x - 1) * a.run, nb = last ? 0 : b + 1;
+        const int nit = last ? it + (int)gridDim.x : it, nb = last ? 0 : b + 1;
         const Source q = source(nit, nb);
         // the scale of the channel this thread stores, ahead of the next weights
         float ws = a.g.ws[min(it * 16 + (int)(threadIdx.x & 15), a.g.N - 1)];
         asm volatile("" : : : "memory");
-        if (b == 0) {
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-                acc[tb] = i32x4{0, 0, 0, 0};
-        }
+        if (b == 0)
+            acc = i32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
             // past the wave's last unit the weights are zero
             const int at = min(wave + (b * kHeld + j) * kI8Waves, units - 1) * kUnit;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int tb = 0; tb < TB; ++tb)
-                    acc[tb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                        w[j][h], *reinterpret_cast<const i32x4 *>(xp[tb] + at + h * 64), acc[tb], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                    w[j][h], *reinterpret_cast<const i32x4 *>(xp + at + h * 64), acc, 0, 0, 0);
                 w[j][h] = load_weight(q, j, h);    // the next step's, into the registers just read
             }
         }
         asm volatile("" : "+v"(ws));     // waited for here, where the count of loads after it is known
         if (last) {
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-                s_red[buf][wave][tb][lane] = acc[tb];
+            s_red[buf][wave][lane] = acc;
             __syncthreads();
             // one output per thread: token i, channel c
-            const int c = threadIdx.x & 15, n = it * 16 + c;
-            for (int i = threadIdx.x >> 4; i < a.g.T && n < a.g.N; i += kI8Threads / 16) {
+            const int i = threadIdx.x >> 4, c = threadIdx.x & 15, n = it * 16 + c;
+            if (i < a.g.T && n < a.g.N) {
                 int sum = 0;
 #pragma unroll
                 for (int v = 0; v < kI8Waves; ++v)
-                    sum += s_red[buf][v][i >> 4][(c >> 2) * 16 + (i & 15)][c & 3];
+                    sum += s_red[buf][v][(c >> 2) * 16 + i][c & 3];
                 ((Ty *)a.g.y)[(size_t)i * a.g.ldy + n] = scaled<Ty>(sum, s_xs[i], ws);
             }
             buf ^= 1;                    // two barriers lie between a buffer's reads and its next writes
@@ -217,45 +194,25 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
     }
 }
 
-template <int TB, class Ty>
-hipError_t run(I8FewArgs a, hipStream_t st)
+template <class Ty>
+hipError_t run(const I8FewArgs &a, hipStream_t st)
 {
-    static LdsAllowed allowed;
     const size_t lds = (size_t)a.g.T * code_stride(a.g.K);
-    const hipError_t err = allow_lds_here(i8_few_kernel<TB, Ty>, lds, allowed);
-    if (err != hipSuccess)
-        return err;
     const int items = (a.g.N + 15) / 16;
-    const int most = lds <= 60 * 1024 ? 512 : 256;         // resident at once
-    // with many turns to share out, two neighbouring blocks a turn: a row's
-    // stores then fill whole cache lines in one L2 (16 tokens, 262144 channels
-    // of fp32: 149 -> 144 us; at 65536 channels the coarser turns cost 1 us)
-    a.run = items >= 16 * most ? 2 : 1;
-    const int turns = (items + a.run - 1) / a.run;
-    i8_few_kernel<TB, Ty><<<dim3(turns < most ? turns : most), dim3(kI8Threads), lds, st>>>(a);
+    const int resident = 512;                    // two workgroups a compute unit
+    i8_few_kernel<Ty><<<dim3(items < resident ? items : resident), dim3(kI8Threads), lds, st>>>(a);
     return hipGetLastError();
 }
 
-template <class Ty>
-hipError_t pick(const I8FewArgs &a, hipStream_t st)
-{
-    return a.g.T <= 16 ? run<1, Ty>(a, st) : run<2, Ty>(a, st);
-}
-
 }  // namespace
-
-bool i8_few_fits(int T, int K)
-{
-    return T <= kI8FewTokens && (size_t)T * code_stride(K) <= 120 * 1024;
-}
 
 hipError_t launch_i8_few(I8FewArgs a, hipStream_t stream)
 {
     const uint32_t pieces = (uint32_t)(code_stride(a.g.K) - 16) / 8;
     a.row_magic = (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
-    return a.g.type == DGW4_F32   ? pick<float>(a, stream)
-           : a.g.type == DGW4_F16 ? pick<_Float16>(a, stream)
-                                  : pick<__bf16>(a, stream);
+    return a.g.type == DGW4_F32   ? run<float>(a, stream)
+           : a.g.type == DGW4_F16 ? run<_Float16>(a, stream)
+                                  : run<__bf16>(a, stream);
 }
 
 }  // namespace dgw4

@@ -1,4 +1,4 @@
-// Products of 8-bit rows over many tokens, y[t, n] = xs[t] ws[n] sum_k xq wq,
+// Products of 8-bit rows, y[t, n] = xs[t] ws[n] sum_k xq wq,
 // in LDS tiles.
 //
 // A workgroup takes BN channels x BT tokens and walks K in stages of 128
@@ -11,7 +11,9 @@
 // chosen by the lane that loads it, so that the 16 rows one MFMA fragment
 // reads at the same K fall on all banks. A lane's offset past K reads as zero
 // (buffer bounds), and rows past T or N repeat the last row, their outputs not
-// stored.
+// stored. A lane stores four channels at once at any alignment: with odd row
+// lengths element stores took 65 us where this takes 37 (1690 tokens, 18679
+// channels of bf16, K = 160), and 313 against 255 at 256 x 262143 x 2816.
 //
 // v_mfma_i32_16x16x64_i8 takes the channels as its row operand: a lane ends
 // with four consecutive channels of one token. The sums are exact, so their
@@ -148,7 +150,6 @@ __global__ void __launch_bounds__(KS *(BN / WN) * (BT / WT) * 64) i8_gemm_kernel
     }
 
     // every scale before the first store: a load behind stores waits for them
-    const bool vec = rows_in_fours<Ty>(a);
     f32x4 ws[NA];
     float xs[NB];
 #pragma unroll
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(KS *(BN / WN) * (BT / WT) * 64) i8_gemm_kernel
             Ty *y = (Ty *)a.y + (size_t)t * a.ldy;
 #pragma unroll
             for (int i = 0; i < NA; ++i)
-                store4<Ty>(y, n0 + wn + i * 16 + 4 * p, a.N, vec, acc[i][j], xs[j], ws[i]);
+                store4<Ty>(y, n0 + wn + i * 16 + 4 * p, a.N, acc[i][j], xs[j], ws[i]);
         }
     }
 }
