@@ -54,7 +54,11 @@ constexpr int kFewRouteTokens = kUpWaves;
 constexpr uint32_t kFewPast = 0x80000000u;   // an offset past every buffer here, small additions included
 
 // Columns of K that one lane-load of packed weights covers are a group G; a
-// wave holds this many groups of weights and activations at once.
+// wave holds up to this many groups of weights and activations at once. The
+// kernels' NB is the least of 1, 2, 3 and so on up to it that holds a wave's
+// share of K: a group past the end costs its arithmetic all the same (26
+// tokens, top-5 of 232, d = 320, m = 1152, g = 64 and 128: 61 -> 31 us; the bits
+// are the same, a wave's groups keep their order).
 template <int G>
 constexpr int kBatch = G == 128 ? 3 : 6;
 template <int G>
@@ -295,10 +299,10 @@ __device__ inline void route_token(const float *__restrict__ l, int E, int topk,
 // every eighth group of d; each weight fragment's registers take the next
 // step's load as soon as it has been used. The scales are staged through LDS,
 // one 16-byte load per thread covers the next item's.
-template <int G, bool TL, bool ROUTED, bool MULTI>
+template <int G, bool TL, bool ROUTED, bool MULTI, int NB>
 __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
 {
-    constexpr int NB = kBatch<G>, W = G / 32;
+    constexpr int W = G / 32;
     __shared__ FewTiles s;
     __shared__ f32x4 s_red[2][kUpWaves][2][64];
     extern __shared__ uint4 s_sc[];      // [2][8 * groups]: s and z of the 16 gate, then of the 16 up rows
@@ -492,10 +496,10 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
 // are sixteen units: every load of the kernel goes out at once.) The scales of
 // the tile's 16 weight rows are contiguous: one 16-byte load per lane (NS of
 // them past 16 groups) into the wave's own slot of LDS.
-template <int G, bool TL, int NS>
+template <int G, bool TL, int NS, int NB>
 __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
-    constexpr int NB = kBatch<G>, W = G / 32;
+    constexpr int W = G / 32;
     __shared__ FewList s;
     __shared__ float s_w[kFewSumInside];
     __shared__ bool s_live[kFewSumInside];
@@ -644,10 +648,10 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 // tile's activations go to LDS (rows 16 bytes off the bank period), then its
 // waves take the tile's column blocks in turn, each streaming all of m past
 // them with the next step's weights loaded as soon as a fragment is used.
-template <int G, bool TL, int NS, bool MULTI>
+template <int G, bool TL, int NS, bool MULTI, int NB>
 __global__ void __launch_bounds__(kUpThreads, 4) few_down_items_kernel(FewArgs a)
 {
-    constexpr int NB = kItemBatch<G>, W = G / 32;
+    constexpr int W = G / 32;
     __shared__ FewList s;
     __shared__ uint4 s_sc[kUpWaves][64 * NS];
     extern __shared__ __attribute__((aligned(16))) char s_h[];     // [16][2 m + 16]
@@ -791,47 +795,55 @@ __global__ void __launch_bounds__(256) few_combine_kernel(FewArgs a)
     *reinterpret_cast<uint2 *>(a.out + (size_t)t * a.d + c) = pack_f16x4(v);
 }
 
-template <int G, bool TL>
-hipError_t run_gate_up(const FewArgs &a, bool routed, hipStream_t st)
+template <int G, bool TL, bool MULTI, int NB>
+hipError_t run_gate_up(const FewArgs &a, hipStream_t st)
 {
     const int items = a.A * (a.m / 16);
     const size_t lds = 2 * 8 * (size_t)(a.d / G) * 16;
     const dim3 grid(items < 512 ? items : 512), block(kUpThreads);
-    const bool multi = a.d / G > kUpWaves * kBatch<G>;
-    if (routed && multi)
-        few_gate_up_kernel<G, TL, true, true><<<grid, block, lds, st>>>(a);
-    else if (routed)
-        few_gate_up_kernel<G, TL, true, false><<<grid, block, lds, st>>>(a);
-    else if (multi)
-        few_gate_up_kernel<G, TL, false, true><<<grid, block, lds, st>>>(a);
+    if (a.logits != nullptr)
+        few_gate_up_kernel<G, TL, true, MULTI, NB><<<grid, block, lds, st>>>(a);
     else
-        few_gate_up_kernel<G, TL, false, false><<<grid, block, lds, st>>>(a);
+        few_gate_up_kernel<G, TL, false, MULTI, NB><<<grid, block, lds, st>>>(a);
     return hipGetLastError();
 }
 
-template <int G, bool TL, int NS>
+template <int G, bool TL>
+hipError_t pick_gate_up(const FewArgs &a, hipStream_t st)
+{
+    const int share = (a.d / G + kUpWaves - 1) / kUpWaves;     // groups of a wave
+    if (share > kBatch<G>)
+        return run_gate_up<G, TL, true, kBatch<G>>(a, st);
+    if (share == 1)
+        return run_gate_up<G, TL, false, 1>(a, st);
+    if (share == 2)
+        return run_gate_up<G, TL, false, 2>(a, st);
+    return share == 3 ? run_gate_up<G, TL, false, 3>(a, st) : run_gate_up<G, TL, false, kBatch<G>>(a, st);
+}
+
+template <int G, bool TL, int NS, int NB>
 hipError_t run_down(const FewArgs &a, hipStream_t st)
 {
     static LdsAllowed allowed;
     const size_t lds = (size_t)a.A * (2 * (size_t)a.m + 16);
-    const hipError_t err = allow_lds_here(few_down_kernel<G, TL, NS>, lds, allowed);
+    const hipError_t err = allow_lds_here(few_down_kernel<G, TL, NS, NB>, lds, allowed);
     if (err != hipSuccess)
         return err;
-    few_down_kernel<G, TL, NS><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
+    few_down_kernel<G, TL, NS, NB><<<dim3(a.d / 16), dim3(kDownThreads), lds, st>>>(a);
     return hipGetLastError();
 }
 
-template <int G, bool TL, int NS, bool MULTI>
+template <int G, bool TL, int NS, bool MULTI, int NB>
 hipError_t run_down_items(const FewArgs &a, hipStream_t st)
 {
     static LdsAllowed allowed;
     const size_t lds = 16 * (2 * (size_t)a.m + 16);
-    hipError_t err = allow_lds_here(few_down_items_kernel<G, TL, NS, MULTI>, lds, allowed);
+    hipError_t err = allow_lds_here(few_down_items_kernel<G, TL, NS, MULTI, NB>, lds, allowed);
     if (err != hipSuccess)
         return err;
     const int items = a.A * (a.d / 16);
     const int groups = (items + kUpWaves - 1) / kUpWaves;
-    few_down_items_kernel<G, TL, NS, MULTI><<<dim3(groups < 512 ? groups : 512), dim3(kUpThreads), lds, st>>>(a);
+    few_down_items_kernel<G, TL, NS, MULTI, NB><<<dim3(groups < 512 ? groups : 512), dim3(kUpThreads), lds, st>>>(a);
     err = hipGetLastError();
     if (err != hipSuccess)
         return err;
@@ -842,13 +854,26 @@ hipError_t run_down_items(const FewArgs &a, hipStream_t st)
 template <int G, bool TL>
 hipError_t pick_down(const FewArgs &a, hipStream_t st)
 {
+    const int groups = a.m / G;
     if (a.y != nullptr) {
-        const int groups = a.m / G;
-        if (groups <= kItemBatch<G>)
-            return run_down_items<G, TL, 1, false>(a, st);
-        return groups <= 16 ? run_down_items<G, TL, 1, true>(a, st) : run_down_items<G, TL, 2, true>(a, st);
+        constexpr int most = kItemBatch<G>;
+        if (groups > most)
+            return groups <= 16 ? run_down_items<G, TL, 1, true, most>(a, st)
+                                : run_down_items<G, TL, 2, true, most>(a, st);
+        if (groups <= 2)
+            return run_down_items<G, TL, 1, false, 2>(a, st);
+        if (groups <= 4)
+            return run_down_items<G, TL, 1, false, 4>(a, st);
+        return groups <= 6 ? run_down_items<G, TL, 1, false, 6>(a, st) : run_down_items<G, TL, 1, false, most>(a, st);
     }
-    return a.m / G <= 16 ? run_down<G, TL, 1>(a, st) : run_down<G, TL, 2>(a, st);
+    const int share = (groups + 1) / 2;
+    if (groups > 16)
+        return run_down<G, TL, 2, kBatch<G>>(a, st);
+    if (share == 1)
+        return run_down<G, TL, 1, 1>(a, st);
+    if (share == 2)
+        return run_down<G, TL, 1, 2>(a, st);
+    return share == 3 ? run_down<G, TL, 1, 3>(a, st) : run_down<G, TL, 1, kBatch<G>>(a, st);
 }
 
 }  // namespace
@@ -863,11 +888,10 @@ bool few_keeps_outputs(int A) { return A > kFewSumInside; }
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream)
 {
     hipError_t err;
-    const bool routed = a.logits != nullptr;
     if (gu_g == 128)
-        err = a.gu_tiled ? run_gate_up<128, true>(a, routed, stream) : run_gate_up<128, false>(a, routed, stream);
+        err = a.gu_tiled ? pick_gate_up<128, true>(a, stream) : pick_gate_up<128, false>(a, stream);
     else
-        err = a.gu_tiled ? run_gate_up<64, true>(a, routed, stream) : run_gate_up<64, false>(a, routed, stream);
+        err = a.gu_tiled ? pick_gate_up<64, true>(a, stream) : pick_gate_up<64, false>(a, stream);
     if (err != hipSuccess)
         return err;
     if (dn_g == 128)
