@@ -77,6 +77,16 @@ SHAPES = [
     dict(T=7, E=200, topk=5, d=128, m=64),
     dict(T=1, E=256, topk=64, d=128, m=64),
     dict(T=64, E=129, topk=1, d=128, m=64),
+    # every number of groups that a wave holds, where K's last share is short
+    dict(T=2, E=4, topk=2, d=1152, m=128, gg=128, dgr=128),
+    dict(T=3, E=4, topk=2, d=1920, m=320, gg=128, dgr=64),
+    dict(T=3, E=4, topk=2, d=576, m=384, gg=64, dgr=128),
+    dict(T=2, E=4, topk=3, d=1472, m=512, gg=64, dgr=128),
+    dict(T=1, E=4, topk=2, d=2112, m=640, gg=64, dgr=128),
+    dict(T=25, E=4, topk=3, d=960, m=320, gg=64, dgr=64),
+    dict(T=25, E=4, topk=3, d=1280, m=512, gg=128, dgr=128),
+    dict(T=22, E=3, topk=3, d=256, m=128, gg=64, dgr=64),
+    dict(T=34, E=3, topk=2, d=1088, m=576, gg=64, dgr=64),
 ]
 
 
