@@ -269,3 +269,29 @@ def test_offsets_past_32_bits():
     q, s = dg.quantize_rows_i8(x)
     rq, rs = few_ref.quantize_rows(x[-3:].cpu())
     assert np.array_equal(q[-3:].cpu().numpy(), rq) and np.array_equal(s[-3:].cpu().numpy(), rs)
+
+
+def test_more_threads_than_a_launch_takes():
+    # rows in two launches; channels past what the smallest tiles' grid can hold
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60 << 30:
+        pytest.skip("needs 60 GiB")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = (1 << 27) + 5
+    x = torch.randint(-3, 4, (rows, 1), dtype=torch.int8, device="cuda", generator=g).half()
+    q, s = dg.quantize_rows_i8(x)
+    # the code of a row's only value is 127 with its sign, or 0
+    assert torch.equal(q[:, 0], (torch.sign(x[:, 0]) * 127).to(torch.int8)) and not q[:, 1:].any()
+    _, rs = few_ref.quantize_rows(torch.arange(4).half()[:, None])
+    assert torch.equal(s, torch.from_numpy(rs).cuda()[x[:, 0].abs().long()])
+    del x, q, s
+    N, K = (1 << 29) + 17, 16
+    wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    ws = torch.rand(N, device="cuda", generator=g)
+    xq = torch.randint(-127, 128, (1, K), dtype=torch.int8, device="cuda", generator=g)
+    xs = torch.rand(1, device="cuda", generator=g)
+    y = dg.w8a8_linear(xq, xs, (wq, ws), dtype=torch.float16)
+    for n0 in (0, N // 2, N - 400):
+        ref = few_ref.product(xq.cpu().numpy(), xs.cpu().numpy(), wq[n0:n0 + 400].cpu().numpy(),
+                              ws[n0:n0 + 400].cpu().numpy(), torch.float16)
+        assert few_ref.same_bits(y[:, n0:n0 + 400], ref), n0

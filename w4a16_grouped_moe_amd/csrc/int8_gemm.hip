@@ -196,13 +196,13 @@ hipError_t run(const I8Args &a, hipStream_t st)
 //   T 256, N 4096, K 2816: 9.8 / 8.4 (64 x 64, two parts)
 //   T 128, N 4096, K 4096: 10.0 / 8.3 (64 x 32, two parts)
 struct I8Tile {
-    int bn, bt;
+    int bn, bt, threads;
     double stage, fixed, per_cu;
 };
 constexpr I8Tile kTiles[] = {
-    {256, 256, 1.80, 8.1, 0.0}, {256, 128, 0.94, 6.1, 0.0}, {128, 128, 0.59, 3.7, 0.0},
-    {64, 128, 0.34, 2.8, 0.0},  {64, 64, 0.24, 1.7, 0.0},   {64, 64, 0.30, 0.9, 1.1},
-    {64, 32, 0.15, 0.8, 0.8},   {32, 32, 0.11, 0.7, 1.0},   {32, 32, 0.093, 1.6, 0.0},
+    {256, 256, 512, 1.80, 8.1, 0.0}, {256, 128, 512, 0.94, 6.1, 0.0}, {128, 128, 512, 0.59, 3.7, 0.0},
+    {64, 128, 512, 0.34, 2.8, 0.0},  {64, 64, 512, 0.24, 1.7, 0.0},   {64, 64, 512, 0.30, 0.9, 1.1},
+    {64, 32, 512, 0.15, 0.8, 0.8},   {32, 32, 512, 0.11, 0.7, 1.0},   {32, 32, 1024, 0.093, 1.6, 0.0},
 };
 
 int pick_tile(const I8Args &a)
@@ -215,7 +215,9 @@ int pick_tile(const I8Args &a)
         const double tiles = (double)((a.N + t.bn - 1) / t.bn) * ((a.T + t.bt - 1) / t.bt) / 256.0;
         const double rounds = t.per_cu == 0.0 ? ceil(tiles) : fmax(1.0, tiles / t.per_cu);
         const double us = (t.fixed + t.stage * stages) * rounds;
-        if (us < least) {
+        // a launch takes fewer than 2^32 threads; the first tile's stay under
+        // that for every y that fits the device
+        if (us < least && (i == 0 || tiles * 256.0 * t.threads < 4294967296.0)) {
             least = us;
             best = i;
         }

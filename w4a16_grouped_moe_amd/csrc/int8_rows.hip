@@ -42,14 +42,20 @@ __global__ void __launch_bounds__(N) quantize_row_kernel(const Tx *__restrict__ 
         s[row] = sc;
 }
 
+// In as many launches as keep one under 2^30 threads (2^32 are refused).
 template <class Tx, int N, int kKept>
 void rows_in(const void *x, int rows, int K, long long ldx, int8_t *q, long long ldq, float *s, hipStream_t st)
 {
-    if constexpr (N <= 64)
-        quantize_rows_kernel<Tx, N, kKept><<<dim3((unsigned)((rows - 1) / (256 / N) + 1)), dim3(256), 0, st>>>(
-            (const Tx *)x, rows, K, ldx, q, ldq, s);
-    else
-        quantize_row_kernel<Tx, N, kKept><<<dim3(rows), dim3(N), 0, st>>>((const Tx *)x, K, ldx, q, ldq, s);
+    constexpr int most = (1 << 30) / N;
+    for (long long at = 0; at < rows; at += most) {
+        const int n = (int)(rows - at < most ? rows - at : most);
+        const Tx *xa = static_cast<const Tx *>(x) + at * ldx;
+        if constexpr (N <= 64)
+            quantize_rows_kernel<Tx, N, kKept><<<dim3((n - 1) / (256 / N) + 1), dim3(256), 0, st>>>(
+                xa, n, K, ldx, q + at * ldq, ldq, s + at);
+        else
+            quantize_row_kernel<Tx, N, kKept><<<dim3(n), dim3(N), 0, st>>>(xa, K, ldx, q + at * ldq, ldq, s + at);
+    }
 }
 
 template <class Tx>
