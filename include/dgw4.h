@@ -411,9 +411,9 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
 
 /*
  * dgw4_moe_few — the routed-expert layer of dgw4_moe_forward for few tokens:
- * at most 512 assignments (T * topk; 64 tokens at top-8). Two launches up to 64
- * assignments (gate_up with its activation; down with the weighted sum), three
- * beyond (the sum apart). Each launch splits the chosen experts' weights over
+ * at most 512 assignments (T * topk; 64 tokens at top-8). Two launches (gate_up
+ * with its activation; down with the weighted sum), or three (the sum apart)
+ * past 64 assignments, or with fewer where d is short or m long for them. Each launch splits the chosen experts' weights over
  * the whole chip, where dgw4_moe_forward gives half an expert to one
  * workgroup: the form for one token to a few dozen (at 128 experts, top-8, d =
  * 2816, m = 704 it is the faster one up to about 24 tokens; past that the two

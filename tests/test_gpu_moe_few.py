@@ -77,6 +77,17 @@ SHAPES = [
     dict(T=7, E=200, topk=5, d=128, m=64),
     dict(T=1, E=256, topk=64, d=128, m=64),
     dict(T=64, E=129, topk=1, d=128, m=64),
+    # up to 64 assignments whose H does not fit down's LDS, or whose down is apart
+    dict(T=6, E=9, topk=8, d=2304, m=1408),
+    dict(T=64, E=4, topk=1, d=2304, m=1024),
+    dict(T=8, E=10, topk=8, d=128, m=2048),
+    dict(T=8, E=9, topk=8, d=512, m=704),
+    dict(T=2, E=9, topk=8, d=1536, m=1408, dgr=128),
+    dict(T=4, E=9, topk=8, d=2304, m=1408),            # 90 KB of H
+    dict(T=8, E=9, topk=8, d=2432, m=704),
+    dict(T=17, E=4, topk=4, d=128, m=4096, dgr=128),   # the longest m
+    dict(T=2, E=5, topk=4, d=256, m=4096, dgr=128),
+    dict(T=2, E=5, topk=4, d=2304, m=4096, dgr=128),
     # every number of groups that a wave holds, where K's last share is short
     dict(T=2, E=4, topk=2, d=1152, m=128, gg=128, dgr=128),
     dict(T=3, E=4, topk=2, d=1920, m=320, gg=128, dgr=64),

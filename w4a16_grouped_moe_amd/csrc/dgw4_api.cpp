@@ -590,7 +590,7 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
         return DGW4_ERR_UNSUPPORTED;
     const size_t h_bytes = round_up(sizeof(uint16_t) * (size_t)A * (size_t)m);
     const size_t id_bytes = round_up(sizeof(int32_t) * (size_t)A);
-    const size_t y_bytes = dgw4::few_keeps_outputs((int)A) ? sizeof(float) * (size_t)A * (size_t)d : 0;
+    const size_t y_bytes = dgw4::few_keeps_outputs((int)A, d, m) ? sizeof(float) * (size_t)A * (size_t)d : 0;
     const size_t list_bytes = A > 0 ? round_up(dgw4::kFewListBytes) : 0;
     const size_t need = h_bytes + 2 * id_bytes + list_bytes + round_up(y_bytes);
     if (!workspace) {
@@ -758,7 +758,7 @@ int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, long long l
     float *xs = reinterpret_cast<float *>(static_cast<char *>(workspace) + q_bytes);
     const dgw4::I8Args a{xq, xs, wq, ws, T, Kp, N, Kp, ldw, ldy, y, y_type};
     if (T <= dgw4::kI8FewTokens && (long long)T * Kp <= dgw4::kI8FewCodes)
-        return from_hip(dgw4::launch_i8_few({a, x, x_type, K, ldx, 0}, (hipStream_t)stream));
+        return from_hip(dgw4::launch_i8_few({a, x, x_type, K, ldx, 0, 0}, (hipStream_t)stream));
     const hipError_t err =
         dgw4::launch_quantize_rows(x, x_type, T, K, ldx, xq, Kp, xs, (hipStream_t)stream);
     if (err != hipSuccess)

@@ -162,10 +162,11 @@ struct FewArgs {
     uint16_t *out;              // fp16 [T, d]
 };
 
-// Up to this many assignments down weights and sums the experts' outputs
-// itself; with more, a third launch does (see moe_few.hip).
+// Up to this many assignments down may weight and sum the experts' outputs
+// itself; else a third launch does, and down leaves them in the workspace (see
+// moe_few.hip).
 constexpr int kFewSumInside = 64;
-bool few_keeps_outputs(int A);
+bool few_keeps_outputs(int A, int d, int m);
 
 // The groups of d and of m the two kernels keep scales for.
 constexpr int kFewMaxUpGroups = 64, kFewMaxDownGroups = 32;
@@ -205,7 +206,8 @@ struct I8FewArgs {
     const void *x;
     int x_type, k_x;
     long long ld;
-    uint32_t row_magic;         // set by launch_i8_few
+    uint32_t row_magic;         // set by launch_i8_few, as is run
+    int run;                    // neighbouring blocks of 16 channels a workgroup takes in turn
 };
 
 hipError_t launch_i8_few(I8FewArgs a, hipStream_t stream);

@@ -6,6 +6,7 @@
 #include "dgw4_internal.hpp"
 
 #include <atomic>
+#include <mutex>
 
 namespace dgw4 {
 namespace {
@@ -209,6 +210,7 @@ hipError_t allow_lds(Kern kern, size_t lds, size_t &allowed)
 constexpr int kMaxDevices = 64;
 struct LdsAllowed {
     std::atomic<size_t> bytes[kMaxDevices] = {};
+    std::mutex raise;                    // two callers at once never lower it
 };
 
 template <class Kern>
@@ -220,6 +222,9 @@ hipError_t allow_lds_here(Kern kern, size_t lds, LdsAllowed &allowed)
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess)
         return err;
+    if (dev < kMaxDevices && lds <= allowed.bytes[dev].load(std::memory_order_relaxed))
+        return hipSuccess;
+    std::lock_guard<std::mutex> lock(allowed.raise);
     if (dev < kMaxDevices && lds <= allowed.bytes[dev].load(std::memory_order_relaxed))
         return hipSuccess;
     err = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

@@ -5,12 +5,12 @@
 //            e = ids[a]; a workgroup takes 16 columns of H for the (at most
 //            16) assignments of one tile at a time and splits d over its
 //            eight waves.
-//   down     out[t, c] = sum_k w[t, k] (H[a] Wd_e^T)[c], k ascending. Up to
-//            kFewSumInside assignments a workgroup takes 16 output columns
-//            for all of them, keeps the experts' outputs in LDS in fp32 and
-//            sums them itself: two launches in all. Beyond, runs of (tile, 16
-//            columns) leave them in fp32 in the workspace and a third launch
-//            sums: at 64 tokens, top-8, a workgroup with 16 columns of every
+//   down     out[t, c] = sum_k w[t, k] (H[a] Wd_e^T)[c], k ascending. With
+//            few assignments (few_keeps_outputs says no) a workgroup takes 16
+//            output columns for all of them, keeps the experts' outputs in LDS
+//            in fp32 and sums them itself: two launches in all. Else runs of
+//            (tile, 16 columns) leave them in fp32 in the workspace and a third
+//            launch sums: at 64 tokens, top-8, a workgroup with 16 columns of every
 //            expert read 2.2 TB/s (64 us), runs of neighbouring columns 4.5
 //            (32 us).
 //
@@ -883,7 +883,17 @@ bool few_routes_inside(int T, int topk, int E)
     return T <= kFewRouteTokens && E <= kFewRouteExperts;
 }
 
-bool few_keeps_outputs(int A) { return A > kFewSumInside; }
+// down sums inside, with a workgroup per 16 columns of the output holding all of
+// H in LDS, where that fits and either the columns alone fill the chip or the
+// work of a workgroup is small. Measured, us a layer, inside / apart: d 2816, m
+// 704, 48 assignments 35.6 / 36.8; d 512, m 704, 16 assignments 15.6 / 16.7, 48
+// assignments 26.2 / 20.4; d 1536, m 1408, 16 assignments 30.4 / 24.7.
+bool few_keeps_outputs(int A, int d, int m)
+{
+    if (A > kFewSumInside || (long long)A * (2LL * m + 16) > 96 * 1024)
+        return true;
+    return d < 2304 && (long long)A * m > 11264 + 4LL * d;
+}
 
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream)
 {
