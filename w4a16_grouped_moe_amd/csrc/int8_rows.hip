@@ -3,8 +3,8 @@
 // by its length.
 //
 // Bound by reading x and writing q once: the row stays in registers between
-// its maximum and its codes (up to 16384 columns). 16001 rows of 2803 bf16: 25.5
-// us (5.3 TB/s; a large device copy moves 4.8 to 5.2 on the same card); 65536
+// its maximum and its codes (up to 16384 columns). 16001 rows of 2803 bf16: 24.3
+// us (5.5 TB/s; a large device copy moves 4.8 to 5.2 on the same card); 65536
 // rows of 64 fp16 5.8 us (a wave per row: 37), 2700 of 16384 bf16 31 (a wave per
 // row, which reads x twice: 53); 256 rows of 2816 fp16 3.3 us, most of it the
 // launch.
