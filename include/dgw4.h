@@ -413,11 +413,12 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
  * dgw4_moe_few — the routed-expert layer of dgw4_moe_forward for few tokens:
  * at most 512 assignments (T * topk; 64 tokens at top-8). Two launches (gate_up
  * with its activation; down with the weighted sum), or three (the sum apart)
- * past 64 assignments, or with fewer where d is short or m long for them. Each launch splits the chosen experts' weights over
- * the whole chip, where dgw4_moe_forward gives half an expert to one
- * workgroup: the form for one token to a few dozen (at 128 experts, top-8, d =
- * 2816, m = 704 it is the faster one up to about 24 tokens; past that the two
- * are within a few per cent).
+ * past 64 assignments, or with fewer where d is short or m long for them. Each
+ * launch splits the chosen experts' weights over the whole chip, where
+ * dgw4_moe_forward gives half an expert to one workgroup: the form for one
+ * token to a few dozen (at 128 experts, top-8, d = 2816, m = 704 it is the
+ * faster one up to about 24 tokens; past that the two are within a few per
+ * cent).
  * The formula, the packed weights in either layout and the treatment of ids
  * (outside [0, E): no contribution; equal ids: each counts) are
  * dgw4_moe_forward's. Sums are fp32, each group's scale applied to an fp32
