@@ -472,7 +472,7 @@ DGW4_API int dgw4_moe_few_routed(const uint16_t *x, const float *router_logits, 
  * product with it is NaN. Exact and deterministic.
  *   x       device, x_type (DGW4_F32, DGW4_F16, DGW4_BF16) [rows, K], rows
  *           ldx elements apart (ldx >= K), aligned to its element
- *   rows >= 0, K >= 1
+ *   rows >= 0, 1 <= K <= 2^31 - 17 (a longer row: INVALID_ARG)
  *   q       device int8 [rows, Kp] (output), Kp = K rounded up to 16, rows
  *           ldq bytes apart (ldq >= Kp, ldq % 16 == 0), 16-byte aligned; columns
  *           K .. Kp - 1 are set to 0, later ones left as they are

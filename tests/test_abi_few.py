@@ -101,6 +101,13 @@ def test_quantize_rows_rejects():
     assert call(rows=0, x=None, q=None, s=None) == B.OK
 
 
+def test_quantize_rows_longest():
+    # the longest row there is room for in 32 bits with its padding, and one more
+    f = dg.lib().dgw4_quantize_rows_i8
+    for K, code in ((2**31 - 17, B.OK), (2**31 - 16, B.ERR_INVALID_ARG)):
+        assert f(None, 1, 0, K, 2**31, None, 2**31, None, None) == code
+
+
 def test_w8a8_rejects():
     f = dg.lib().dgw4_w8a8_linear
     ok = dict(xq=P, xs=P, T=4, K=64, ldx=64, wq=P, ws=P, N=5, ldw=64, y=P, t=1, ldy=5)

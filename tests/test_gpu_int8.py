@@ -295,3 +295,31 @@ def test_more_threads_than_a_launch_takes():
         ref = few_ref.product(xq.cpu().numpy(), xs.cpu().numpy(), wq[n0:n0 + 400].cpu().numpy(),
                               ws[n0:n0 + 400].cpu().numpy(), torch.float16)
         assert few_ref.same_bits(y[:, n0:n0 + 400], ref), n0
+
+
+def test_longest_row():
+    # the most columns a row may have: the last step of every thread passes 2^31.
+    # Codes against the definition in fp32, over the whole row and with the row's
+    # maximum in its last column; the memory around them stays
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    K, pad = 2**31 - 17, 1 << 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty((1, K), dtype=torch.float16, device="cuda").normal_(generator=g)
+    x[0, K - 1] = -200
+    big = torch.full((K + 1 + 2 * pad,), 55, dtype=torch.int8, device="cuda")
+    q, s = big[pad:pad + K + 1].view(1, K + 1), torch.empty(1, device="cuda")
+    dg.quantize_rows_i8(x, out=(q, s))
+    torch.cuda.synchronize()
+    scale = np.float32(200) / np.float32(127)
+    assert s.item() == scale
+    assert (big[:pad] == 55).all() and (big[pad + K + 1:] == 55).all() and q[0, K] == 0
+    step = 1 << 26
+    for k in range(0, K, step):
+        # the quotient in 64 bits rounded to 32 is the one of fp32
+        want = torch.round((x[0, k:k + step].double() / s.double()).float()).clamp_(-127, 127).to(torch.int8)
+        assert torch.equal(q[0, k:min(k + step, K)], want), k
+    for part in (slice(0, 20000), slice(K - 20000, K)):     # and by the host's division
+        want = np.rint(x[0, part].float().cpu().numpy() / scale)
+        assert np.array_equal(q[0, part].cpu().numpy(), want.astype(np.int8))

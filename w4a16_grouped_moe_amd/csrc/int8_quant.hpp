@@ -10,6 +10,7 @@
 // lane) with a value nearer to one divide.
 #pragma once
 
+#include "int8_columns.hpp"
 #include "int8_common.hpp"
 
 namespace dgw4 {
@@ -184,8 +185,8 @@ __device__ inline float quantize_row(const Tx *__restrict__ row, int K, int end,
 #pragma unroll
     for (int j = 0; j < kKept; ++j)
         top = max(top, top8(v[j]));
-    for (int k = (kKept * N + tid) * 8; k < K; k += N * 8)
-        top = max(top, top8(load8<Tx>(row, k, K)));
+    const int rest = (kKept * N + tid) * 8;
+    each_column<N * 8>(rest, K, [&](int k) { top = max(top, top8(load8<Tx>(row, k, K))); });
     top = lanes_top<(N < 64 ? N : 64)>(top);
     if constexpr (N > 64) {
         if ((tid & 63) == 0)
@@ -202,8 +203,9 @@ __device__ inline float quantize_row(const Tx *__restrict__ row, int K, int end,
         if (k < end)
             *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(v[j], rs);
     }
-    for (int k = (kKept * N + tid) * 8; k < end; k += N * 8)
+    each_column<N * 8>(rest, end, [&](int k) {
         *reinterpret_cast<uint2 *>(q + k) = codes8<Tx>(load8<Tx>(row, k, K), rs);
+    });
     return rs.s;
 }
 
