@@ -164,6 +164,29 @@ def test_binding_rejects_host_tensors():
         dg.quantize_rows_i8([[1.0]])
 
 
+def test_binding_refuses_sizes_past_32_bits():
+    # the C ABI takes 32-bit sizes: a larger one is refused, not taken modulo 2^32
+    big = 2**32 + 1
+    for shape in ((big, 16), (1, big), (2**31, 1)):
+        t = torch.empty(shape, dtype=torch.int8, device="meta")
+        with pytest.raises(ValueError, match="32 bits"):
+            B._rows(t, "x", B._I8, t.get_device())
+    edge = torch.empty((1, 2**31 - 1), dtype=torch.int8, device="meta")
+    assert B._rows(edge, "x", B._I8, edge.get_device())[1:3] == (1, 2**31 - 1)
+    for args in ((big, 8, 128, 2816, 704), (1, big, 128, 2816, 704), (1, 8, big, 2816, 704),
+                 (1, 8, 128, 2816 + 2**32, 704), (1, 8, 128, 2816, 704 - 2**32),
+                 (1, 8, 128, 2816, 704, 2**32 + 128), (1, 8, 128, 2816, 704, 128, 2**32 + 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dg.moe_few_workspace_bytes(*args)
+    for T, K in ((big, 16), (1, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dg.w8a8_workspace_bytes(T, K)
+    x, lg = torch.zeros((1, 64), dtype=torch.float16), torch.zeros((1, 4))
+    w = (torch.zeros((4, 2, 2), dtype=torch.uint8),)
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.moe_few_routed(x, lg, 2**32 + 2, w, w)
+
+
 def test_plain_form_agrees_with_the_oracle():
     # the 64-bit form the GPU tests use, against the oracle's layer
     rng = np.random.default_rng(1)

@@ -323,3 +323,17 @@ def test_longest_row():
     for part in (slice(0, 20000), slice(K - 20000, K)):     # and by the host's division
         want = np.rint(x[0, part].float().cpu().numpy() / scale)
         assert np.array_equal(q[0, part].cpu().numpy(), want.astype(np.int8))
+
+
+def test_more_rows_than_32_bits():
+    # refused, whatever the memory holds (as 2^32 + 3 rows modulo 2^32 it would
+    # be three)
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    x = torch.zeros((2**32 + 3, 1), dtype=torch.float16, device="cuda")
+    w = (torch.zeros((4, 16), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda"))
+    out = (torch.zeros((3, 16), dtype=torch.int8, device="cuda"), torch.zeros(3, device="cuda"))
+    for call in (lambda: dg.quantize_rows_i8(x, out=out), lambda: dg.w8a8_linear_tokens(x, w)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()

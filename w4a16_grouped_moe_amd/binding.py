@@ -506,9 +506,18 @@ def moe_forward_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, 
 
 
 
+def _sizes(**sizes) -> None:
+    """The C ABI's sizes are 32-bit integers, and ctypes takes larger ones
+    modulo 2^32: refuse those here."""
+    for name, v in sizes.items():
+        if not -2**31 <= v < 2**31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def moe_few_workspace_bytes(T: int, topk: int, E: int, d: int, m: int, gu_g: int = 128,
                             dn_g: int = 64) -> int:
     """Device workspace moe_few and moe_few_routed need (host-only query)."""
+    _sizes(T=T, topk=topk, E=E, d=d, m=m, gu_g=gu_g, dn_g=dn_g)
     n = ctypes.c_size_t(0)
     _check("dgw4_moe_few(query)", lib().dgw4_moe_few(
         None, None, None, T, topk, E, d, m, None, None, None, gu_g, None, None, None, dn_g,
@@ -583,6 +592,8 @@ def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, o
     if gshape != (E, 2 * m, d // 2) or dq.shape != (E, d, m // 2):
         raise ValueError(f"packed shapes {tuple(gq.shape)} / {tuple(dq.shape)} do not match "
                          f"x {tuple(x.shape)}")
+    if (gg | dg) >> 31:
+        _sizes(gu_g=gg, dn_g=dg)
     if _group(gg) < 1 or _group(dg) < 1:
         raise ValueError("group sizes must be positive")
     if gs.shape != (E, m2, d // _group(gg)) or gz.shape != gs.shape:
@@ -625,6 +636,7 @@ def moe_few_routed(x: torch.Tensor, router_logits: torch.Tensor, topk: int, gu: 
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_few from router logits fp32 [T, E]: the same bits as router()
     followed by moe_few()."""
+    _sizes(topk=topk)
     if router_logits.shape != (x.shape[0], gu[0].shape[0]):
         raise ValueError("router_logits must be [T, E]")
     return _few("dgw4_moe_few_routed", x, ((router_logits, "router_logits", (torch.float32,)),),
@@ -642,6 +654,8 @@ def _rows(t: torch.Tensor, name: str, dtypes, d: int) -> tuple[int, int, int, in
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
+    if (rows | cols) >> 31:
+        _sizes(**{f"rows of {name}": rows, f"columns of {name}": cols})
     ld, step = t.stride()
     if rows <= 1:
         ld = cols
@@ -711,6 +725,7 @@ def w8a8_linear(xq: torch.Tensor, xs: torch.Tensor, w: tuple, out: torch.Tensor 
 
 def w8a8_workspace_bytes(T: int, K: int) -> int:
     """Device workspace w8a8_linear_tokens needs (host-only query)."""
+    _sizes(T=T, K=K)
     n = ctypes.c_size_t(0)
     _check("dgw4_w8a8_linear_tokens(query)", lib().dgw4_w8a8_linear_tokens(
         None, 0, T, K, K, None, None, 1, _up16(K), None, 0, 1, None, ctypes.byref(n), None))
