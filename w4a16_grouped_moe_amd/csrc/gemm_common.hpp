@@ -213,10 +213,17 @@ struct LdsAllowed {
     std::mutex raise;                    // two callers at once never lower it
 };
 
+// A launch with more LDS than this, static and dynamic, has to be allowed first.
+// Kernels that use allow_lds_here keep their static part below kLdsStatic
+// (each asserts it), and dynamic sizes up to the difference need no call.
+constexpr size_t kLdsUnasked = 64 * 1024;
+constexpr size_t kLdsStatic = 48 * 1024;
+constexpr size_t kLdsDynamicUnasked = kLdsUnasked - kLdsStatic;
+
 template <class Kern>
 hipError_t allow_lds_here(Kern kern, size_t lds, LdsAllowed &allowed)
 {
-    if (lds <= 16 * 1024)
+    if (lds <= kLdsDynamicUnasked)
         return hipSuccess;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);

@@ -74,8 +74,8 @@ struct FewList {
 };
 static_assert(sizeof(FewList) == kFewListBytes && sizeof(FewList) % 16 == 0, "copied in 16-byte pieces");
 
-// One workgroup's list and what it is built with.
-struct FewTiles : FewList {
+// What a workgroup builds its list with.
+struct FewBuild {
     int32_t id[kFewMaxAssign];           // each assignment's expert, -1 if none
     int count[kMaxExperts];              // assignments of each expert
     uint32_t base[kMaxExperts];          // first tile << 16 | first row of each expert
@@ -102,14 +102,14 @@ __device__ inline int tile_expert_of(uint32_t t) { return (int)(t & 0x3FF); }
 __device__ inline int tile_start_of(uint32_t t) { return (int)(t >> 10 & 0x3FF); }
 __device__ inline int tile_rows_of(uint32_t t) { return (int)(t >> 20); }
 
-// The list from s.id (A entries, written before the last barrier), for up to
+// The list from b.id (A entries, written before the last barrier), for up to
 // 64 assignments: lane a of the first wave gathers the mask of the
 // assignments with its expert. 16 row slots per tile.
-__device__ inline void build_tiles_small(FewTiles &s, int A, int topk)
+__device__ inline void build_tiles_small(FewList &s, const FewBuild &b, int A, int topk)
 {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
-        const int id = lane < A ? s.id[lane] : -1;
+        const int id = lane < A ? b.id[lane] : -1;
         uint64_t same = 0;
         for (int i = 0; i < A; ++i)
             same |= (uint64_t)(id == __builtin_amdgcn_readlane(id, i)) << i;
@@ -137,23 +137,23 @@ __device__ inline void build_tiles_small(FewTiles &s, int A, int topk)
 
 // The list for any number of assignments: LDS counters and a scan over the
 // experts.
-__device__ inline void build_tiles_any(FewTiles &s, int A, int topk, int E)
+__device__ inline void build_tiles_any(FewList &s, FewBuild &b, int A, int topk, int E)
 {
     const int tid = threadIdx.x;
     for (int e = tid; e < E; e += blockDim.x)
-        s.count[e] = 0;
+        b.count[e] = 0;
     __syncthreads();
-    const int id = tid < A ? s.id[tid] : -1;
+    const int id = tid < A ? b.id[tid] : -1;
     const bool live = id >= 0;
     int rank = 0;
     if (live)
-        rank = atomicAdd(&s.count[id], 1);
+        rank = atomicAdd(&b.count[id], 1);
     __syncthreads();
-    if (live && s.count[id] > 16) {
+    if (live && b.count[id] > 16) {
         // several tiles: the rank by ascending assignment
         rank = 0;
         for (int j = 0; j < tid; ++j)
-            rank += s.id[j] == id;
+            rank += b.id[j] == id;
     }
     if (tid < 64) {
         // one wave: `per` consecutive experts per lane, then a wave scan
@@ -161,7 +161,7 @@ __device__ inline void build_tiles_any(FewTiles &s, int A, int topk, int E)
         uint32_t sum = 0;
         for (int j = 0; j < per; ++j) {
             const int e = tid * per + j;
-            const int c = e < E ? s.count[e] : 0;
+            const int c = e < E ? b.count[e] : 0;
             sum += (uint32_t)((c + 15) / 16) << 16 | (uint32_t)c;
         }
         uint32_t inc = sum;
@@ -174,8 +174,8 @@ __device__ inline void build_tiles_any(FewTiles &s, int A, int topk, int E)
         for (int j = 0; j < per; ++j) {
             const int e = tid * per + j;
             if (e < E) {
-                const int c = s.count[e];
-                s.base[e] = at;
+                const int c = b.count[e];
+                b.base[e] = at;
                 at += (uint32_t)((c + 15) / 16) << 16 | (uint32_t)c;
             }
         }
@@ -184,24 +184,24 @@ __device__ inline void build_tiles_any(FewTiles &s, int A, int topk, int E)
     }
     __syncthreads();
     if (live) {
-        const uint32_t b = s.base[id];
-        const int start = (int)(b & 0xFFFF);
+        const uint32_t at = b.base[id];
+        const int start = (int)(at & 0xFFFF);
         s.row[start + rank] = (uint32_t)tid | (uint32_t)(tid / topk) << 16;
         if (rank % 16 == 0)
-            s.tile[(b >> 16) + rank / 16] = (uint32_t)id | (uint32_t)(start + rank) << 10 |
-                                            (uint32_t)min(16, s.count[id] - rank) << 20;
+            s.tile[(at >> 16) + rank / 16] = (uint32_t)id | (uint32_t)(start + rank) << 10 |
+                                            (uint32_t)min(16, b.count[id] - rank) << 20;
     }
     __syncthreads();
 }
 
-// The list from s.id, ids outside [0, E) as -1: they belong to no tile.
-__device__ inline void build_tiles(FewTiles &s, int A, int topk, int E)
+// The list from b.id, ids outside [0, E) as -1: they belong to no tile.
+__device__ inline void build_tiles(FewList &s, FewBuild &b, int A, int topk, int E)
 {
     __syncthreads();
     if (A <= kSmallAssign)
-        build_tiles_small(s, A, topk);
+        build_tiles_small(s, b, A, topk);
     else
-        build_tiles_any(s, A, topk, E);
+        build_tiles_any(s, b, A, topk, E);
 }
 
 // The first launch's list for the second (building it again takes 1 to 2.2 us).
@@ -303,8 +303,15 @@ template <int G, bool TL, bool ROUTED, bool MULTI, int NB>
 __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
 {
     constexpr int W = G / 32;
-    __shared__ FewTiles s;
-    __shared__ f32x4 s_red[2][kUpWaves][2][64];
+    __shared__ FewList s;
+    __shared__ union {
+        FewBuild build;                  // until the list is done
+        f32x4 red[2][kUpWaves][2][64];   // after the barrier ahead of the items
+    } s_u;
+    auto &s_red = s_u.red;
+    static_assert(sizeof(s) + sizeof(s_u) <= kLdsStatic &&
+                      2 * 8 * kFewMaxUpGroups * sizeof(uint4) <= kLdsDynamicUnasked,
+                  "launched without an allowance");
     extern __shared__ uint4 s_sc[];      // [2][8 * groups]: s and z of the 16 gate, then of the 16 up rows
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -319,15 +326,15 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
             int32_t *ids = a.rids + t * a.topk;
             float *w = a.rw + t * a.topk;
             if (a.E <= 128)
-                route_token<2>(l, a.E, a.topk, s.id + t * a.topk, ids, w, blockIdx.x == 0);
+                route_token<2>(l, a.E, a.topk, s_u.build.id + t * a.topk, ids, w, blockIdx.x == 0);
             else
-                route_token<kFewRouteExperts / 64>(l, a.E, a.topk, s.id + t * a.topk, ids, w, blockIdx.x == 0);
+                route_token<kFewRouteExperts / 64>(l, a.E, a.topk, s_u.build.id + t * a.topk, ids, w, blockIdx.x == 0);
         }
     } else if (tid < a.A) {
         const int id = a.ids[tid];
-        s.id[tid] = id >= 0 && id < a.E ? id : -1;
+        s_u.build.id[tid] = id >= 0 && id < a.E ? id : -1;
     }
-    build_tiles(s, a.A, a.topk, a.E);
+    build_tiles(s, s_u.build, a.A, a.topk, a.E);
     if (blockIdx.x == 0)
         publish_list(s, a.list);
     const int items = uniform(s.tiles) * cblocks;
@@ -505,6 +512,8 @@ __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
     __shared__ bool s_live[kFewSumInside];
     __shared__ float s_y[2][kFewSumInside][16];
     __shared__ uint4 s_sc[kDownWaves][64 * NS];
+    static_assert(sizeof(s) + sizeof(s_w) + sizeof(s_live) + sizeof(s_y) + sizeof(s_sc) <= kLdsStatic,
+                  "allow_lds_here's limit");
     extern __shared__ __attribute__((aligned(16))) char s_h[];     // [A][2 m + 16]
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -654,6 +663,7 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_down_items_kernel(FewArgs a
     constexpr int W = G / 32;
     __shared__ FewList s;
     __shared__ uint4 s_sc[kUpWaves][64 * NS];
+    static_assert(sizeof(s) + sizeof(s_sc) <= kLdsStatic, "allow_lds_here's limit");
     extern __shared__ __attribute__((aligned(16))) char s_h[];     // [16][2 m + 16]
     const int tid = threadIdx.x;
     const int lane = tid & 63;
