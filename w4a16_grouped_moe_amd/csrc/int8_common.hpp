@@ -79,7 +79,7 @@ __device__ inline void copy_to_lds(rsrc_t r, uint32_t voff, uint32_t lds)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(r)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // All of this wave's LDS reads have returned and at most N of its copies are
