@@ -220,6 +220,45 @@ def test_activations_strided_and_nonfinite(T):
     assert (big[T] == 3).all() and (big[:, :2] == 3).all() and (big[:, 72:] == 3).all()
 
 
+# 512 workgroups take 16 channels at a time: a few that take a second turn,
+# several whole rounds, several batches of K a turn, and both sides of the size
+# (16384 blocks of channels) from which a turn is two neighbouring blocks, with
+# an odd last one
+@pytest.mark.parametrize("T,K,N", [(1, 600, 8193), (5, 300, 8200), (6, 1000, 8208), (6, 2900, 24603),
+                                   (1, 9000, 16401), (5, 3600, 24590), (2, 6500, 9000), (6, 64, 57361),
+                                   (1, 600, 262128), (6, 600, 262129), (5, 600, 262145), (5, 3600, 262149),
+                                   (6, 80, 524305)])
+def test_few_tokens_in_turns(T, K, N):
+    g = torch.Generator(device="cuda").manual_seed(N + T)
+    x = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    wq = torch.randint(-127, 128, (N, (K + 15) // 16 * 16), dtype=torch.int8, device="cuda", generator=g)
+    ws = torch.rand(N, device="cuda", generator=g) + 0.5
+    q, s = dg.quantize_rows_i8(x)
+    rq, rs = few_ref.quantize_rows(x.cpu())
+    for dtype in TYPES:
+        y = dg.w8a8_linear_tokens(x, (wq, ws), dtype=dtype)
+        assert few_ref.same_bits(y, dg.w8a8_linear(q, s, (wq, ws), dtype=dtype)), dtype
+        for n0 in (0, 8192 - 40, N // 2, N - 80):
+            n1 = min(N, n0 + 80)
+            ref = few_ref.product(rq, rs, wq[n0:n1].cpu().numpy(), ws[n0:n1].cpu().numpy(), dtype)
+            assert few_ref.same_bits(y[:, n0:n1], ref), (dtype, n0)
+    # into rows that lie apart, replayed: what lies between stays
+    big = torch.full((T + 1, N + 7), 3.0, device="cuda")
+    ws_buf = torch.empty(dg.w8a8_workspace_bytes(T, K), dtype=torch.uint8, device="cuda")
+    out = big[:T, 3:3 + N]
+    want = dg.w8a8_linear(q, s, (wq, ws), dtype=torch.float32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.w8a8_linear_tokens(x, (wq, ws), out=out, workspace=ws_buf)
+    for _ in range(3):
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert few_ref.same_bits(out, want)
+    assert (big[T] == 3).all() and (big[:, :3] == 3).all() and (big[:, 3 + N:] == 3).all()
+
+
 def test_empty_batch():
     w = (torch.zeros((8, 32), dtype=torch.int8, device="cuda"), torch.ones(8, device="cuda"))
     assert dg.w8a8_linear(w[0][:0], w[1][:0], w).shape == (0, 8)
