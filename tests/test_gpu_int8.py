@@ -148,6 +148,13 @@ def test_product_tiles(T, K, N):
         assert few_ref.same_bits(y, few_ref.product(xq, xs, wq, ws, dtype))
 
 
+# the tiles with K in two and four parts that few sizes reach
+@pytest.mark.parametrize("T,K,N", [(250, 2816, 4001), (180, 4000, 4099), (256, 2560, 4095), (40, 8192, 35),
+                                   (33, 10240, 90), (95, 9104, 70)])
+def test_product_tiles_in_parts(T, K, N):
+    test_product_tiles(T, K, N)
+
+
 @pytest.mark.parametrize("T", [1, 9, 70, 300])
 def test_product_extremes(T):
     # the largest sums (all codes -128 at the longest K), zeros, and scales
