@@ -187,6 +187,14 @@ def test_binding_refuses_sizes_past_32_bits():
         dg.moe_few_routed(x, lg, 2**32 + 2, w, w)
 
 
+def test_binding_refuses_an_empty_workspace():
+    none, one = torch.empty(0, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        B._workspace(none, 1, none.get_device())
+    B._workspace(none, 0, none.get_device())
+    assert B._workspace(one, 1, one.get_device())[0] == one.data_ptr()
+
+
 def test_plain_form_agrees_with_the_oracle():
     # the 64-bit form the GPU tests use, against the oracle's layer
     rng = np.random.default_rng(1)

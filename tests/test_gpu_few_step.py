@@ -112,3 +112,20 @@ def test_steps_on_two_streams():
                 got[i] = m.step(xs[i], bufs[i])
     torch.cuda.synchronize()
     assert _same(got[0], want[0]) and _same(got[1], want[1])
+
+
+def test_empty_workspace():
+    # a workspace without bytes is an error, not the size query that a NULL one
+    # is in the C ABI; for no tokens it is enough
+    m = Model()
+    x = torch.randn((2, D), device="cuda").half()
+    lg = torch.randn((2, E), device="cuda")
+    ids, w = dg.router(lg, TOPK)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    calls = [lambda n: dg.w8a8_linear_tokens(x[:n], m.proj, workspace=none),
+             lambda n: dg.moe_few(x[:n], ids[:n], w[:n], m.gu, m.dn, workspace=none),
+             lambda n: dg.moe_few_routed(x[:n], lg[:n], TOPK, m.gu, m.dn, workspace=none)]
+    for call in calls:
+        with pytest.raises(ValueError, match="workspace"):
+            call(2)
+        assert call(0).shape == (0, D)

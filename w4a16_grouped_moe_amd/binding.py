@@ -561,6 +561,16 @@ def _flat(t, name: str, dtypes, d: int) -> int:
     return t.data_ptr()
 
 
+def _workspace(t, T: int, d: int) -> tuple:
+    """Pointer and size of a workspace for T tokens on device d. One without
+    bytes has no pointer, which the C ABI takes for the size query: it would
+    return without an error and without a launch."""
+    p = _flat(t, "workspace", _U8, d)
+    if not p and T > 0:
+        raise ValueError("workspace is empty")
+    return p, ctypes.byref(ctypes.c_size_t(t.numel()))
+
+
 def _call(fn: str, d: int, *args) -> None:
     """Enqueue one call on device d's current stream, with that device the
     current one for the call."""
@@ -611,7 +621,7 @@ def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, o
           T, topk, E, d, m,
           _flat(gq, "gu_q", _U8, d_), _flat(gs, "gu_s", _F16, d_), _flat(gz, "gu_z", _F16, d_), gg,
           _flat(dq, "dn_q", _U8, d_), _flat(ds, "dn_s", _F16, d_), _flat(dz, "dn_z", _F16, d_), dg,
-          _flat(workspace, "workspace", _U8, d_), ctypes.byref(ctypes.c_size_t(workspace.numel())),
+          *_workspace(workspace, T, d_),
           _flat(out, "out", _F16, d_))
     return out
 
@@ -751,6 +761,5 @@ def w8a8_linear_tokens(x: torch.Tensor, w: tuple, out: torch.Tensor | None = Non
     if workspace is None:
         workspace = x.new_empty(max(w8a8_workspace_bytes(T, K), 1), dtype=torch.uint8)
     _call("dgw4_w8a8_linear_tokens", d, px, _TYPES[x.dtype], T, K, ldx, pw, pws, N, ldw, py,
-          _TYPES[out.dtype], ldy, _flat(workspace, "workspace", _U8, d),
-          ctypes.byref(ctypes.c_size_t(workspace.numel())))
+          _TYPES[out.dtype], ldy, *_workspace(workspace, T, d))
     return out
