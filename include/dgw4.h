@@ -416,14 +416,16 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
  * past 64 assignments, or with fewer where d is short or m long for them. Each
  * launch splits the chosen experts' weights over the whole chip, where
  * dgw4_moe_forward gives half an expert to one workgroup: the form for one
- * token to a few dozen (at 128 experts, top-8, d = 2816, m = 704 it is the
- * faster one up to about 24 tokens; past that the two are within a few per
- * cent).
+ * token to a few dozen (at 128 experts, top-8, d = 2816, m = 704, tiled
+ * weights it is the faster one up to about 24 tokens, and up to 6% slower from
+ * there to 64; with d = 6144 and 64 experts 16% slower at 64 tokens, with d =
+ * 2048 and m = 1408 26% faster). Nothing chooses between the two: the caller
+ * does.
  * The formula, the packed weights in either layout and the treatment of ids
  * (outside [0, E): no contribution; equal ids: each counts) are
  * dgw4_moe_forward's. Sums are fp32, each group's scale applied to an fp32
  * partial sum of exact integers times x; the gated intermediate is rounded to
- * fp16 once, the expert outputs stay in fp32 until they are weighted and added
+ * fp16 once (past 65504 it is infinite, as in dgw4_moe_forward), the expert outputs stay in fp32 until they are weighted and added
  * in ascending k, and out is rounded to fp16 once. The results agree with
  * dgw4_moe_forward's up to rounding and repeated calls give identical bits. A
  * row of x enters its own token's results only; a token without live ids gets

@@ -628,8 +628,8 @@ def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, o
 
 def moe_few(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, gu: tuple, dn: tuple,
             workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
-    """The routed-expert layer for few tokens (T * topk <= 512), in two
-    launches that split the chosen experts' weights over the whole chip.
+    """The routed-expert layer for few tokens (T * topk <= 512), in two or
+    three launches that split the chosen experts' weights over the whole chip.
 
     Arguments as for moe_forward (see dgw4_moe_few in include/dgw4.h);
     ``workspace``: uint8 of at least moe_few_workspace_bytes(...), allocated

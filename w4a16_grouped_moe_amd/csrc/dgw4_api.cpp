@@ -636,7 +636,7 @@ int moe_few_impl(const uint16_t *x, const int32_t *topk_ids, const float *topk_w
     if (routed) {
         int32_t *rids = reinterpret_cast<int32_t *>(ws + h_bytes);
         float *rw = reinterpret_cast<float *>(ws + h_bytes + id_bytes);
-        if (dgw4::few_routes_inside(T, topk, E)) {
+        if (dgw4::few_routes_inside(T, E)) {
             a.logits = router_logits;
             a.rids = rids;
             a.rw = rw;

@@ -172,10 +172,10 @@ bool few_keeps_outputs(int A, int d, int m);
 constexpr int kFewMaxUpGroups = 64, kFewMaxDownGroups = 32;
 
 // Whether launch_few takes a.logits itself; else the router runs before it.
-bool few_routes_inside(int T, int topk, int E);
+bool few_routes_inside(int T, int E);
 hipError_t launch_few(const FewArgs &a, int gu_g, int dn_g, hipStream_t stream);
 
-// 8-bit rows and products (int8.hip). Types as DGW4_F32, DGW4_F16, DGW4_BF16.
+// 8-bit rows and products (int8_rows.hip, int8_gemm.hip). Types as DGW4_F32, DGW4_F16, DGW4_BF16.
 hipError_t launch_quantize_rows(const void *x, int type, int rows, int K, long long ldx, int8_t *q,
                                 long long ldq, float *s, hipStream_t stream);
 

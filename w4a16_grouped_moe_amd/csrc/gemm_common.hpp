@@ -73,10 +73,11 @@ __device__ constexpr uint32_t wq_group_off(int gi)
 }
 
 // NT: non-temporal (cache policy nt). Only for the tiled layout, whose loads
-// cover whole lines, and only where no other workgroup will read the same
-// weights (an expert with a single tile): the canonical layout's loads cover
-// half or quarter lines whose rest the next group's load reads, and the
-// other tiles of a busy expert re-read its weights from the caches.
+// cover whole lines: the canonical layout's loads cover half or quarter lines
+// whose rest the next group's load reads. It suits weights that no other
+// workgroup will read (an expert with a single tile), since the other tiles of
+// a busy expert re-read its weights from the caches; the few-token layer, where
+// nearly every expert has one tile, sets it for all.
 template <int G, bool NT>
 __device__ inline Frag<G> load_frag(rsrc_t r, uint32_t voff, uint32_t soff)
 {

@@ -188,7 +188,9 @@ __global__ void __launch_bounds__(kI8Threads, 4) i8_few_kernel(I8FewArgs a)
                     sum += s_red[buf][v][(c >> 2) * 16 + i][c & 3];
                 ((Ty *)a.g.y)[(size_t)i * a.g.ldy + n] = scaled<Ty>(sum, s_xs[i], ws);
             }
-            buf ^= 1;                    // two barriers lie between a buffer's reads and its next writes
+            // one barrier lies between a buffer's reads and its next writes: the
+            // next item's, which no thread passes before all have read this one
+            buf ^= 1;
         }
         it = nit;
         b = nb;

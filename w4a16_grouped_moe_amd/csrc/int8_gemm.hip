@@ -26,7 +26,8 @@
 // products: the power the chip may draw bounds them, and deeper pipelines (four
 // stages of 64 bytes), fragments held a half stage ahead, waves that only copy
 // (with the tiles of a run overlapping their stores) and smaller tiles two to
-// a CU all measured the same or slower.
+// a CU all measured the same or slower. That is of the largest tile: the smaller
+// ones' stages were not made deeper.
 #include "int8_common.hpp"
 #include "int8_tiles.hpp"
 

@@ -17,11 +17,16 @@
 // Each product's fp32 accumulators are rounded once to fp16 where H is stored
 // (16-bit activations, as everywhere in this library's layer).
 //
-// The layer is bound by the experts' weights, read once each, so the launches
-// split the weights over the whole chip (44 column blocks per expert in
-// gate_up, 176 in down at m = 704, d = 2816) where the 32-row-tile kernel
-// gives a whole half expert to one workgroup: at one token, eight experts,
-// that kernel keeps 16 of the 256 compute units busy (64 us; 16.5 here).
+// The layer is bound by the experts' weights, read once for each tile of up to
+// 16 assignments (once each, where no expert has more), so the launches split
+// them over the whole chip (44 column blocks per expert in gate_up at m = 704,
+// 176 in down at d = 2816) where the 32-row-tile kernel gives a whole half
+// expert to one workgroup: at one token, eight experts, that kernel keeps 16 of
+// the 256 compute units busy (64 us; 16.5 here).
+// Tiled weights are read non-temporally, also by an expert's second and later
+// tiles: at 128 experts most have one (64 tokens 84 us, 93 without). 8 experts,
+// top-2, take 17.9 us at 16 tokens and 50 at 256, four tiles or more an expert,
+// where one read of their weights is 5.
 // Measured at 128 experts, top-8, d = 2816, m = 704, tiled weights, back to
 // back in a graph: 1 token 16.5 us (gate_up 10.6, down 6.8 alone), 4 tokens
 // 34, 16 tokens 61, 64 tokens 83 (gate_up 46, down 32, the sum 4: gate_up reads
@@ -434,6 +439,9 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
     for (int b = 0; cur.left > 0;) {
         const uint32_t tile = tile_at(s, cur.tile);
         const int n = tile_rows_of(tile), start = tile_start_of(tile);
+        // at a change of tile, and at every step where a wave's share of K takes
+        // several (MULTI): these loads are behind the step's weights, which the
+        // wait for them drains (d = 6144, 64 experts: 25.6 us at one token, 128 at 64)
         if (have != cur.tile * batches + b) {
             have = cur.tile * batches + b;
             load_x(tile, b);
@@ -502,7 +510,10 @@ __global__ void __launch_bounds__(kUpThreads, 4) few_gate_up_kernel(FewArgs a)
 // fragment's registers as soon as it has been used. (One token's eight tiles
 // are sixteen units: every load of the kernel goes out at once.) The scales of
 // the tile's 16 weight rows are contiguous: one 16-byte load per lane (NS of
-// them past 16 groups) into the wave's own slot of LDS.
+// them past 16 groups) into the wave's own slot of LDS. With NS = 2 the compiler
+// keeps them in scratch (48 bytes a lane, here and in few_down_items_kernel) and
+// each step waits for all its loads: d = m = 2048, 64 experts, 25.8 us at one
+// token.
 template <int G, bool TL, int NS, int NB>
 __global__ void __launch_bounds__(kDownThreads) few_down_kernel(FewArgs a)
 {
@@ -888,14 +899,15 @@ hipError_t pick_down(const FewArgs &a, hipStream_t st)
 
 }  // namespace
 
-bool few_routes_inside(int T, int topk, int E)
+bool few_routes_inside(int T, int E)
 {
     return T <= kFewRouteTokens && E <= kFewRouteExperts;
 }
 
-// down sums inside, with a workgroup per 16 columns of the output holding all of
-// H in LDS, where that fits and either the columns alone fill the chip or the
-// work of a workgroup is small. Measured, us a layer, inside / apart: d 2816, m
+// Whether down leaves the experts' outputs in the workspace, to be summed by a
+// launch of their own. It does not (and sums inside, a workgroup per 16 columns
+// of the output holding all of H in LDS) where H fits and either the columns
+// alone fill the chip or the work of a workgroup is small. Measured, us a layer, inside / apart: d 2816, m
 // 704, 48 assignments 35.6 / 36.8; d 512, m 704, 16 assignments 15.6 / 16.7, 48
 // assignments 26.2 / 20.4; d 1536, m 1408, 16 assignments 30.4 / 24.7.
 bool few_keeps_outputs(int A, int d, int m)
