@@ -425,11 +425,11 @@ DGW4_API int dgw4_sample_noalloc(const float *logits, int R, int V, uint64_t see
  * (outside [0, E): no contribution; equal ids: each counts) are
  * dgw4_moe_forward's. Sums are fp32, each group's scale applied to an fp32
  * partial sum of exact integers times x; the gated intermediate is rounded to
- * fp16 once (past 65504 it is infinite, as in dgw4_moe_forward), the expert outputs stay in fp32 until they are weighted and added
- * in ascending k, and out is rounded to fp16 once. The results agree with
- * dgw4_moe_forward's up to rounding and repeated calls give identical bits. A
- * row of x enters its own token's results only; a token without live ids gets
- * zeros.
+ * fp16 once (past 65504 it is infinite, as in dgw4_moe_forward), the expert
+ * outputs stay in fp32 until they are weighted and added in ascending k, and out
+ * is rounded to fp16 once. The results agree with dgw4_moe_forward's up to
+ * rounding and repeated calls give identical bits. A row of x enters its own
+ * token's results only; a token without live ids gets zeros.
  *   T >= 0, 1 <= topk <= E, 1 <= E <= 1024, d % gu_g == 0, m % dn_g == 0;
  *   gu_g, dn_g: 64 or 128, each or-ed with DGW4_WEIGHTS_TILED where that
  *   stack is tiled; the DGW4_ROWS_* bits are refused (INVALID_ARG).
