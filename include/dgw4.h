@@ -528,6 +528,130 @@ DGW4_API int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, lo
                                      size_t *ws_bytes, void *stream);
 
 /*
+ * dgw4_w4a16_linear_few — the dense layer of dgw4_w4a16_linear for few tokens
+ * (1 to 64: projections and the LM head of a serving step):
+ *   y[t, n] = sum over groups j of s[n, j] * (sum_k q[n, k] x[t, k] - z[n, j] sum_k x[t, k])
+ * k over the group's g weights. The weights are read once, by the whole chip;
+ * x and y may be of other types and row distances than dgw4_w4a16_linear's, N
+ * need not be a multiple of 16, and K may have any number of groups.
+ * Sums are fp32: codes enter as the exact values 16 + q, the group's
+ * (16 + z) sum_k x is taken off its sum, the scale is applied to the
+ * difference; y is rounded to its type once. Results do not depend on timing,
+ * repeated calls give identical bits, and a token's results depend on its own
+ * row of x only. A token with a NaN or an infinity in x has NaN or infinite
+ * results; finite ones below 2^100 cannot overflow on the way.
+ *   x   device, x_type DGW4_F16 or DGW4_BF16 [T, K], rows ldx elements apart
+ *       (ldx >= K), aligned to its element
+ *   q, s, z, g  one matrix [N, K] as for dgw4_w4a16_linear (16-byte aligned;
+ *       K % g == 0; g 64 or 128, or-ed with DGW4_WEIGHTS_TILED where q is
+ *       tiled, N % 16 == 0 then; the DGW4_ROWS_* bits are refused); z any
+ *       finite fp16
+ *   y   device, y_type (DGW4_F32, DGW4_F16, DGW4_BF16) [T, N] (output), rows
+ *       ldy elements apart (ldy >= N), aligned to its element; elements
+ *       between the rows are left as they are. x and y must not overlap.
+ *   T >= 0 (T == 0 is a no-op), N >= 1, K >= 64.
+ * DGW4_ERR_UNSUPPORTED for T > 64, other group sizes, x_type DGW4_F32,
+ * K > 2^24 or N > 2^31 - 257; DGW4_ERR_INVALID_ARG for the rest. Enqueued on
+ * `stream`, no host sync.
+ */
+DGW4_API int dgw4_w4a16_linear_few(const void *x, int x_type, int T, int K, long long ldx,
+                                   const uint8_t *q, const uint16_t *s, const uint16_t *z, int N,
+                                   int g, void *y, int y_type, long long ldy, void *stream);
+
+/*
+ * The rules that a batch of requests puts on its logits. Row r of the logits
+ * belongs to sequence i = row_seq[r]. A logit l of token v goes through, each
+ * operation rounded to fp32:
+ *   v among tokens[i, 0 .. n), n = lengths[i]:
+ *              l = l > 0 ? l / repetition[i] : l * repetition[i]
+ *   v c times among tokens[i, p .. n), p = prompt_lengths[i] (the generated
+ *   ones), c > 0:
+ *              l = l - frequency[i] * c, then l = l - presence[i]
+ *   v in bias_ids[i, :] at place j (the last such place): l = l + bias[i, j]
+ *              l = l * scale[i]   (one over a temperature)
+ *   v not allowed by the row's mask: l = -inf, whatever it was
+ * Everything here is a host struct of device pointers; the struct is read
+ * during the call, the arrays when the kernels run. An absent rule is a NULL
+ * pointer. Values in the arrays are not checked: a token or a bias id outside
+ * [0, V) is skipped, lengths are taken within [0, max_tokens], prompt lengths
+ * within [0, lengths], penalties and scales as they are.
+ *   sequences   number of sequences the per-sequence arrays hold, >= 0
+ *   row_seq     int32 [R]; outside [0, sequences): the row has no rules but
+ *               its mask. NULL: row r is sequence r (sequences >= R, or 0)
+ *   tokens      int32 [sequences, max_tokens], rows ld_tokens apart; NULL:
+ *               none, and no penalties then. 1 <= max_tokens < 2^21
+ *   lengths     int32 [sequences]; prompt_lengths int32 [sequences] or NULL
+ *               (0: all tokens count as generated)
+ *   repetition, frequency, presence, scale   fp32 [sequences] or NULL
+ *   n_bias, bias_ids, bias   int32 and fp32 [sequences, n_bias], rows ld_bias
+ *               apart; 0 <= n_bias < 1024 (more: DGW4_ERR_UNSUPPORTED); 0: none
+ *   mask        uint32 [mask_rows, ceil(V / 32)], rows ld_mask words apart:
+ *               bit v % 32 of word v / 32 set: v is allowed; or NULL
+ *   mask_row    int32 [R], the row's row of mask; outside [0, mask_rows): the
+ *               row has no mask. NULL: row r has mask row r (mask_rows >= R)
+ * All arrays are aligned to their elements.
+ */
+typedef struct {
+    const int32_t *row_seq;
+    const int32_t *tokens;
+    const int32_t *lengths;
+    const int32_t *prompt_lengths;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const float *scale;
+    const int32_t *bias_ids;
+    const float *bias;
+    const uint32_t *mask;
+    const int32_t *mask_row;
+    long long ld_tokens;
+    long long ld_bias;
+    long long ld_mask;
+    int sequences;
+    int max_tokens;
+    int n_bias;
+    int mask_rows;
+} dgw4_logit_rules;
+
+/*
+ * dgw4_adjust_logits — the rules on R rows of V logits.
+ *   logits  device, type (DGW4_F32, DGW4_F16, DGW4_BF16) [R, V], rows ld
+ *           elements apart (ld >= V), aligned to its element; any values
+ *   out     device, out_type (DGW4_F32 or `type`) [R, V] (output), rows ld_out
+ *           elements apart, aligned to its element; rounded to its type once;
+ *           elements between the rows are left as they are. out == logits
+ *           with the same type and row distance is the call in place (what no
+ *           rule changes is not written then); else the rows must not overlap
+ *           (DGW4_ERR_INVALID_ARG)
+ *   R >= 0 (0: a no-op), 1 <= V < 2^30 and R * V < 2^40 (more:
+ *   DGW4_ERR_UNSUPPORTED)
+ * Bit-exact and deterministic. Enqueued on `stream`, no host sync.
+ */
+DGW4_API int dgw4_adjust_logits(const void *logits, int type, int R, int V, long long ld,
+                                const dgw4_logit_rules *rules, void *out, int out_type,
+                                long long ld_out, void *stream);
+
+/*
+ * dgw4_sample_adjusted — dgw4_sample on the logits that dgw4_adjust_logits
+ * would give in fp32, in one pass over the original ones: entropy fp32 [R],
+ * sample int32 [R] (the noise of dgw4_sample for the same row, token and
+ * seed) and argmax int32 [R], each may be NULL. Adjusted logits have to be
+ * finite or -inf (what the mask takes out may have been anything). A row
+ * where everything is -inf has entropy 0, sample -1 and argmax -1.
+ * Logits, rules and limits as for dgw4_adjust_logits; V need not be a
+ * multiple of 4. The logits are only read.
+ *   workspace  device scratch of *ws_bytes bytes, 16-byte aligned, this call's
+ *       own; workspace == NULL writes the required size, which goes by R and V
+ *       alone, to *ws_bytes and launches nothing
+ * The sample and argmax are those of the adjusted logits bit for bit; every
+ * reduction has a fixed order, and repeated calls give identical bits.
+ */
+DGW4_API int dgw4_sample_adjusted(const void *logits, int type, int R, int V, long long ld,
+                                  const dgw4_logit_rules *rules, uint64_t seed, float *entropy,
+                                  int32_t *sample, int32_t *argmax, void *workspace,
+                                  size_t *ws_bytes, void *stream);
+
+/*
  * dgw4_hbm_read_probe — a measurement aid, not a step of the layer: reads
  * `bytes` bytes of device memory at `buf` once, with the whole chip
  * (16-byte non-temporal loads, several in flight per lane), so that the elapsed time on

@@ -95,6 +95,13 @@ def lib():
         L.dgw4_w8a8_linear_tokens.restype = I
         L.dgw4_w8a8_linear_tokens.argtypes = [P, I, I, I, LL, P, P, I, LL, P, I, LL, P,
                                               ctypes.POINTER(S), P]
+        L.dgw4_w4a16_linear_few.restype = I
+        L.dgw4_w4a16_linear_few.argtypes = [P, I, I, I, LL, P, P, P, I, I, P, I, LL, P]
+        L.dgw4_adjust_logits.restype = I
+        L.dgw4_adjust_logits.argtypes = [P, I, I, I, LL, P, P, I, LL, P]
+        L.dgw4_sample_adjusted.restype = I
+        L.dgw4_sample_adjusted.argtypes = [P, I, I, I, LL, P, ctypes.c_uint64, P, P, P, P,
+                                           ctypes.POINTER(S), P]
         L.dgw4_hbm_read_probe.restype = I
         L.dgw4_hbm_read_probe.argtypes = [P, S, P, P]
         L.dgw4_mfma_probe.restype = I
@@ -585,6 +592,7 @@ def _call(fn: str, d: int, *args) -> None:
 
 
 _U8, _I32, _F32, _I8 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.int8,)
+_HALVES, _MASKS = (torch.float16, torch.bfloat16), (torch.int32, torch.uint32)
 
 
 def _few(fn: str, x, route: tuple, topk: int, gu: tuple, dn: tuple, workspace, out) -> torch.Tensor:
@@ -763,3 +771,178 @@ def w8a8_linear_tokens(x: torch.Tensor, w: tuple, out: torch.Tensor | None = Non
     _call("dgw4_w8a8_linear_tokens", d, px, _TYPES[x.dtype], T, K, ldx, pw, pws, N, ldw, py,
           _TYPES[out.dtype], ldy, *_workspace(workspace, T, d))
     return out
+
+
+def w4a16_linear_few(x: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
+                     dtype: torch.dtype | None = None) -> torch.Tensor:
+    """The dense W4A16 linear for 1 to 64 tokens: y = x * deq(W)^T.
+
+    x fp16 or bf16 [T, K] (rows may lie apart); w = (q uint8 [N, K/2], s fp16
+    [N, K/g], z fp16 [N, K/g], g) as for w4a16_linear, any N, or its pack_tiled
+    form. Returns y [T, N] of ``dtype`` (fp16, bf16 or fp32; x's type when not
+    given), or written into ``out``, whose type counts then. See
+    dgw4_w4a16_linear_few in include/dgw4.h."""
+    q, s, z, g = w
+    d = _gpu(x, "x")
+    px, T, K, ldx = _rows(x, "x", _HALVES, d)
+    if g >> 31 or _group(g) < 1:
+        raise ValueError(f"group size {g} with its flags is not valid")
+    pq, ps, pz = _flat(q, "q", _U8, d), _flat(s, "s", _F16, d), _flat(z, "z", _F16, d)
+    N = q.shape[0]
+    if q.shape != (N, K // 2) or s.shape != (N, K // _group(g)) or z.shape != s.shape:
+        raise ValueError(f"packed shapes {tuple(q.shape)}, {tuple(s.shape)}, {tuple(z.shape)} do not match "
+                         f"x {tuple(x.shape)}")
+    if N >> 31:
+        _sizes(N=N)
+    out, py, ldy = _w8a8_out(x, T, N, dtype or x.dtype, out, d)
+    _call("dgw4_w4a16_linear_few", d, px, _TYPES[x.dtype], T, K, ldx, pq, ps, pz, N, g, py,
+          _TYPES[out.dtype], ldy)
+    return out
+
+
+class _Rules(ctypes.Structure):
+    """dgw4_logit_rules."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("row_seq", "tokens", "lengths", "prompt_lengths",
+                                                "repetition", "frequency", "presence", "scale",
+                                                "bias_ids", "bias", "mask", "mask_row")] +
+                [(n, ctypes.c_longlong) for n in ("ld_tokens", "ld_bias", "ld_mask")] +
+                [(n, ctypes.c_int) for n in ("sequences", "max_tokens", "n_bias", "mask_rows")])
+
+
+class LogitRules:
+    """The rules that a batch of requests puts on its logits (dgw4_logit_rules
+    in include/dgw4.h, which has their order): made once for a batch, checked
+    here. It keeps the tensors it is given, and every call reads what they hold
+    then, so a step appends tokens, moves lengths on or writes a new mask in
+    place.
+
+    tokens int32 [S, max_tokens], lengths and prompt_lengths int32 [S] (the
+    prompt's tokens come first; without prompt_lengths all count as
+    generated); repetition, frequency, presence, scale fp32 [S]; bias_ids
+    int32 and bias fp32 [S, n] (an id outside the vocabulary is an unused
+    place); mask int32 or uint32 [M, words of 32 tokens] (a set bit: allowed);
+    row_seq and mask_row int32, a row's sequence and its row of mask, for at
+    least as many rows as the logits have (without them row r has sequence r
+    and mask row r). Rows of the 2-d tensors may lie apart. Each may be left
+    out."""
+    __slots__ = ("_c", "_ref", "_kept", "_d", "_words", "_rows")
+
+    def __init__(self, tokens=None, lengths=None, prompt_lengths=None, repetition=None,
+                 frequency=None, presence=None, scale=None, bias_ids=None, bias=None, mask=None,
+                 mask_row=None, row_seq=None):
+        self._kept = tuple(t for t in (tokens, lengths, prompt_lengths, repetition, frequency, presence,
+                                       scale, bias_ids, bias, mask, mask_row, row_seq) if t is not None)
+        self._d = d = _gpu(self._kept[0], "a rule's tensor") if self._kept else -1
+        self._c = c = _Rules()
+        self._ref = ctypes.byref(c)
+        if (tokens is None) != (lengths is None):
+            raise ValueError("tokens and lengths go together")
+        if (bias_ids is None) != (bias is None):
+            raise ValueError("bias_ids and bias go together")
+        if tokens is None and not (prompt_lengths is repetition is frequency is presence is None):
+            raise ValueError("penalties and prompt_lengths need tokens")
+        if mask is None and mask_row is not None:
+            raise ValueError("mask_row needs mask")
+        S = None
+        for name, t, types in (("lengths", lengths, _I32), ("prompt_lengths", prompt_lengths, _I32),
+                               ("repetition", repetition, _F32), ("frequency", frequency, _F32),
+                               ("presence", presence, _F32), ("scale", scale, _F32)):
+            if t is not None:
+                setattr(c, name, _flat(t, name, types, d))
+                if t.dim() != 1 or S not in (None, t.shape[0]):
+                    raise ValueError(f"{name} must be [S], one value per sequence")
+                S = t.shape[0]
+        if tokens is not None:
+            c.tokens, n, c.max_tokens, c.ld_tokens = _rows(tokens, "tokens", _I32, d)
+            if n != S or c.max_tokens < 1:
+                raise ValueError(f"tokens must be [{S}, max_tokens], max_tokens at least 1")
+        if bias is not None:
+            c.bias, n, c.n_bias, c.ld_bias = _rows(bias, "bias", _F32, d)
+            c.bias_ids, *ids = _rows(bias_ids, "bias_ids", _I32, d)
+            if ids[:2] != [n, c.n_bias] or S not in (None, n):
+                raise ValueError("bias_ids and bias must both be [S, n]")
+            if ids[2] != c.ld_bias:
+                raise ValueError("bias_ids and bias must have the same row distance")
+            S = n
+        self._words, self._rows = 0, []          # the columns of mask, and how many rows the rules reach
+        if row_seq is not None:
+            c.row_seq = _flat(row_seq, "row_seq", _I32, d)
+            self._rows.append(("row_seq", row_seq.numel()))
+        elif S is not None:
+            self._rows.append(("sequences", S))
+        if mask is not None:
+            c.mask, c.mask_rows, self._words, c.ld_mask = _rows(mask, "mask", _MASKS, d)
+            if mask_row is not None:
+                c.mask_row = _flat(mask_row, "mask_row", _I32, d)
+                self._rows.append(("mask_row", mask_row.numel()))
+            else:
+                self._rows.append(("mask", c.mask_rows))
+        c.sequences = S or 0
+        if c.sequences != (S or 0):
+            _sizes(sequences=S)
+
+
+def _logits(logits, rules, d: int) -> tuple:
+    """Pointer, type, rows, columns and row distance of a batch's logits that
+    the rules are for."""
+    p, R, V, ld = _rows(logits, "logits", _TYPES, d)
+    if not isinstance(rules, LogitRules):
+        raise TypeError("rules must be LogitRules")
+    if rules._d != d and rules._kept:
+        raise ValueError(f"the rules are on cuda:{rules._d}, the logits on cuda:{d}")
+    for name, n in rules._rows:
+        if n < R:
+            raise ValueError(f"{name}: the rules reach {n} rows, the logits have {R}")
+    if rules._words * 32 < V and rules._c.mask:
+        raise ValueError(f"mask has {rules._words} words a row, {V} columns need {(V + 31) // 32}")
+    return p, _TYPES[logits.dtype], R, V, ld
+
+
+def adjust_logits(logits: torch.Tensor, rules: LogitRules, out: torch.Tensor | None = None,
+                  dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The rules' penalties, biases, scale and masks on logits [R, V] (fp32,
+    fp16 or bf16; rows may lie apart), each row by its sequence.
+
+    Returns the adjusted logits [R, V] of ``dtype`` (fp32, or the logits' own),
+    or written into ``out``, whose type counts then; ``out=logits`` is the call
+    in place. See dgw4_adjust_logits in include/dgw4.h."""
+    d = _gpu(logits, "logits")
+    args = _logits(logits, rules, d)
+    R, V = args[2:4]
+    out, po, ldo = _w8a8_out(logits, R, V, dtype, out, d)
+    if R:
+        _call("dgw4_adjust_logits", d, *args, rules._ref, po, _TYPES[out.dtype], ldo)
+    return out
+
+
+def sample_adjusted_workspace_bytes(R: int, V: int) -> int:
+    """Device workspace sample_adjusted needs (host-only query)."""
+    _sizes(R=R, V=V)
+    n = ctypes.c_size_t(0)
+    _check("dgw4_sample_adjusted(query)", lib().dgw4_sample_adjusted(
+        None, 0, R, V, V, None, 0, None, None, None, None, ctypes.byref(n), None))
+    return int(n.value)
+
+
+def sample_adjusted(logits: torch.Tensor, rules: LogitRules, seed: int = 0, entropy: bool = True,
+                    draw: bool = True, workspace: torch.Tensor | None = None):
+    """sample() on the logits that adjust_logits() would give in fp32, in one
+    pass over the original ones [R, V] (fp32, fp16 or bf16, any V; rows may lie
+    apart): (entropy fp32 [R] or None, sample int32 [R] or None, argmax int32
+    [R]). A row that the rules leave nothing of has entropy 0 and -1 for
+    both tokens. ``workspace``: uint8 of at least
+    sample_adjusted_workspace_bytes(R, V), allocated here when not given. See
+    dgw4_sample_adjusted in include/dgw4.h."""
+    d = _gpu(logits, "logits")
+    args = _logits(logits, rules, d)
+    R, V = args[2:4]
+    if workspace is None:
+        workspace = logits.new_empty(max(sample_adjusted_workspace_bytes(R, V), 1), dtype=torch.uint8)
+    h = logits.new_empty(R, dtype=torch.float32) if entropy else None
+    smp = logits.new_empty(R, dtype=torch.int32) if draw else None
+    am = logits.new_empty(R, dtype=torch.int32)
+    if R:
+        _call("dgw4_sample_adjusted", d, *args, rules._ref, int(seed) & (2**64 - 1),
+              h.data_ptr() if entropy else None, smp.data_ptr() if draw else None, am.data_ptr(),
+              *_workspace(workspace, R, d))
+    return h, smp, am

@@ -658,6 +658,11 @@ size_t type_bytes(int type)
     return type == DGW4_F32 ? 4 : type == DGW4_F16 || type == DGW4_BF16 ? 2 : 0;
 }
 
+constexpr int kMaxKFew = 1 << 24;           // K of the few-token W4A16 product
+constexpr int kMaxColumns = 1 << 30;        // of a row of logits
+constexpr int kMaxBias = 1 << 10;           // biases of a sequence: a place fits ten bits
+constexpr int kMaxTokens = 1 << 21;         // tokens of a sequence: a count fits 21 bits
+
 constexpr int kMaxK8 = 131056;              // K * 128 * 128 < 2^31
 constexpr long long kMaxLd8 = 1LL << 22;    // row distances the products address
 
@@ -786,6 +791,150 @@ int dgw4_sample(const float *logits, int R, int V, uint64_t seed, float *entropy
         return DGW4_ERR_INVALID_ARG;
     return from_hip(dgw4::launch_sample(logits, R, V, seed, entropy, sample, argmax, workspace,
                                         (hipStream_t)stream));
+}
+
+int dgw4_w4a16_linear_few(const void *x, int x_type, int T, int K, long long ldx, const uint8_t *q,
+                          const uint16_t *s, const uint16_t *z, int N, int garg, void *y, int y_type,
+                          long long ldy, void *stream)
+{
+    int g = 0, tiled = 0;
+    if (!split_group(garg, g, tiled) || g < 1)
+        return DGW4_ERR_INVALID_ARG;
+    if (T < 0 || K < 1 || N < 1 || type_bytes(x_type) == 0 || type_bytes(y_type) == 0 || ldx < K || ldy < N)
+        return DGW4_ERR_INVALID_ARG;
+    if (!group_supported(g) || x_type == DGW4_F32)
+        return DGW4_ERR_UNSUPPORTED;
+    if (K % g != 0 || (tiled && N % 16 != 0))
+        return DGW4_ERR_INVALID_ARG;
+    if (T > dgw4::kW4FewTokens || K > kMaxKFew || N > INT_MAX - 256)
+        return DGW4_ERR_UNSUPPORTED;
+    if (T == 0)
+        return DGW4_OK;
+    if (!x || !q || !s || !z || !y || !aligned(x, type_bytes(x_type)) || !aligned(q, 16) || !aligned(s, 16) ||
+        !aligned(z, 16) || !aligned(y, type_bytes(y_type)))
+        return DGW4_ERR_INVALID_ARG;
+    const dgw4::W4FewArgs a{x, q, s, z, y, ldx, ldy, T, K, N, x_type, y_type, tiled};
+    return from_hip(dgw4::launch_w4_few(a, g, (hipStream_t)stream));
+}
+
+namespace {
+
+// The checks that the calls on a batch's logits share, before any device
+// pointer of theirs is looked at (R = 0 needs none).
+int logits_sizes(int type, int R, int V, long long ld, const dgw4_logit_rules *u)
+{
+    if (R < 0 || V < 1 || type_bytes(type) == 0 || ld < V || !u)
+        return DGW4_ERR_INVALID_ARG;
+    if (u->sequences < 0 || u->n_bias < 0 || u->mask_rows < 0)
+        return DGW4_ERR_INVALID_ARG;
+    if (V >= kMaxColumns || (long long)R * V >= (1LL << 40) || u->n_bias >= kMaxBias)
+        return DGW4_ERR_UNSUPPORTED;
+    const bool penalties = u->repetition || u->frequency || u->presence;
+    const bool per_sequence = u->tokens || penalties || u->scale || u->n_bias > 0;
+    if (per_sequence && !u->row_seq && u->sequences != 0 && u->sequences < R)
+        return DGW4_ERR_INVALID_ARG;
+    if (u->tokens ? !u->lengths || u->max_tokens < 1 || u->ld_tokens < u->max_tokens : penalties)
+        return DGW4_ERR_INVALID_ARG;
+    if (u->tokens && u->max_tokens >= kMaxTokens)
+        return DGW4_ERR_UNSUPPORTED;
+    if (u->n_bias > 0 && (!u->bias_ids || !u->bias || u->ld_bias < u->n_bias))
+        return DGW4_ERR_INVALID_ARG;
+    if (u->mask && (u->ld_mask < (V + 31) / 32 || (!u->mask_row && u->mask_rows < R)))
+        return DGW4_ERR_INVALID_ARG;
+    const void *words[] = {u->row_seq,  u->tokens, u->lengths,  u->prompt_lengths, u->repetition, u->frequency,
+                           u->presence, u->scale,  u->bias_ids, u->bias,           u->mask,       u->mask_row};
+    for (const void *p : words)
+        if (!aligned(p, 4))
+            return DGW4_ERR_INVALID_ARG;
+    return DGW4_OK;
+}
+
+// Whether rows [R, V] at a (ea bytes an element, rows lda apart) and at b touch:
+// with one row distance they may lie between each other, else their spans are
+// compared.
+bool rows_touch(const void *a, size_t ea, long long lda, const void *b, size_t eb, long long ldb, int R, int V)
+{
+    const unsigned __int128 x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const unsigned __int128 na = (unsigned __int128)(R - 1) * lda * ea + (unsigned __int128)V * ea;
+    const unsigned __int128 nb = (unsigned __int128)(R - 1) * ldb * eb + (unsigned __int128)V * eb;
+    if (!(x < y + nb && y < x + na))
+        return false;
+    const unsigned __int128 d = (unsigned __int128)lda * ea;
+    if (R == 1 || d != (unsigned __int128)ldb * eb)
+        return true;
+    const unsigned __int128 off = y >= x ? (y - x) % d : (d - (x - y) % d) % d;
+    return off < (unsigned __int128)V * ea || off + (unsigned __int128)V * eb > d;
+}
+
+}  // namespace
+
+int dgw4_adjust_logits(const void *logits, int type, int R, int V, long long ld, const dgw4_logit_rules *rules,
+                       void *out, int out_type, long long ld_out, void *stream)
+{
+    if (type_bytes(out_type) == 0 || ld_out < V)
+        return DGW4_ERR_INVALID_ARG;
+    const int st = logits_sizes(type, R, V, ld, rules);
+    if (st != DGW4_OK)
+        return st;
+    if (out_type != type && out_type != DGW4_F32)
+        return DGW4_ERR_UNSUPPORTED;
+    if (R == 0)
+        return DGW4_OK;
+    if (!logits || !out || !aligned(logits, type_bytes(type)) || !aligned(out, type_bytes(out_type)))
+        return DGW4_ERR_INVALID_ARG;
+    const bool in_place = out == logits && type == out_type && (ld == ld_out || R == 1);
+    if (!in_place && rows_touch(logits, type_bytes(type), ld, out, type_bytes(out_type), ld_out, R, V))
+        return DGW4_ERR_INVALID_ARG;
+    dgw4::LogitArgs a{};
+    a.rules = *rules;
+    a.logits = logits;
+    a.out = out;
+    a.ld = ld;
+    a.ld_out = ld_out;
+    a.R = R;
+    a.V = V;
+    a.type = type;
+    a.out_type = out_type;
+    return from_hip(dgw4::launch_adjust_logits(a, (hipStream_t)stream));
+}
+
+int dgw4_sample_adjusted(const void *logits, int type, int R, int V, long long ld, const dgw4_logit_rules *rules,
+                         uint64_t seed, float *entropy, int32_t *sample, int32_t *argmax, void *workspace,
+                         size_t *ws_bytes, void *stream)
+{
+    if (!ws_bytes || R < 0 || V < 1)
+        return DGW4_ERR_INVALID_ARG;
+    if (V >= kMaxColumns || (long long)R * V >= (1LL << 40))
+        return DGW4_ERR_UNSUPPORTED;
+    const size_t need = dgw4::sample_adjusted_workspace_bytes(R, V);
+    if (!workspace) {
+        *ws_bytes = need;
+        return DGW4_OK;
+    }
+    const int st = logits_sizes(type, R, V, ld, rules);
+    if (st != DGW4_OK)
+        return st;
+    if (*ws_bytes < need)
+        return DGW4_ERR_WORKSPACE;
+    if (R == 0)
+        return DGW4_OK;
+    if (!logits || !aligned(logits, type_bytes(type)) || !aligned(workspace, 16) || !aligned(entropy, 4) ||
+        !aligned(sample, 4) || !aligned(argmax, 4))
+        return DGW4_ERR_INVALID_ARG;
+    dgw4::LogitArgs a{};
+    a.rules = *rules;
+    a.logits = logits;
+    a.parts = workspace;
+    a.entropy = entropy;
+    a.sample = sample;
+    a.argmax = argmax;
+    a.ld = ld;
+    a.R = R;
+    a.V = V;
+    a.type = type;
+    a.k0 = (uint32_t)seed;
+    a.k1 = (uint32_t)(seed >> 32);
+    return from_hip(dgw4::launch_sample_adjusted(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "gemm_common.hpp"
+#include "element_types.hpp"
 
 #include "dgw4.h"
 
@@ -13,23 +14,6 @@ namespace {
 #pragma clang fp contract(off)
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-__device__ inline float to_f32(float v) { return v; }
-__device__ inline float to_f32(_Float16 v) { return (float)v; }
-__device__ inline float to_f32(__bf16 v)
-{
-    return __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(uint16_t, v) << 16);
-}
-
-// v rounded to Ty. The empty asm keeps the fp32 rounding of the product before
-// it: the compiler would otherwise form the product and its fp16 rounding in
-// one v_fma_mixlo_f16.
-template <class Ty>
-__device__ inline Ty from_f32(float v)
-{
-    asm("" : "+v"(v));
-    return (Ty)v;
-}
 
 // One output: the integer sum, rounded to fp32, times the token's scale, times
 // the channel's, each product rounded, then rounded to Ty.

@@ -21,7 +21,7 @@
 // the workspace; a second kernel merges a row's partials in ascending split
 // order. Every reduction has a fixed order, so results are bitwise
 // reproducible.
-#include "dgw4_internal.hpp"
+#include "sampler_common.hpp"
 
 #include <climits>
 #include <mutex>
@@ -32,91 +32,7 @@ namespace {
 constexpr int kSmpThreads = 256;
 constexpr int kSmpUnroll = 4;                      // float4 loads in flight per thread
 
-struct Partial {
-    float m, z, s;                                 // max, sum exp(l - m), sum exp(l - m) * (l - m)
-    float av;                                      // argmax value and index
-    int ai;
-    float sv;                                      // best Gumbel score and index
-    int si;
-    int pad;
-};
-static_assert(sizeof(Partial) == 32, "partial layout");
-
 typedef float f32x4v __attribute__((ext_vector_type(4)));
-
-__device__ inline void philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
-                                     uint32_t k1, uint32_t (&out)[4])
-{
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        if (r > 0) {
-            k0 += 0x9E3779B9u;
-            k1 += 0xBB67AE85u;
-        }
-        // each full 64-bit product in one v_mad_u64_u32 (instead of a
-        // separate high and low multiply, both quarter rate)
-        const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
-        const uint32_t h0 = (uint32_t)(p0 >> 32), l0 = (uint32_t)p0;
-        const uint32_t h1 = (uint32_t)(p1 >> 32), l1 = (uint32_t)p1;
-        const uint32_t n0 = h1 ^ c1 ^ k0, n2 = h0 ^ c3 ^ k1;
-        c0 = n0;
-        c1 = l1;
-        c2 = n2;
-        c3 = l0;
-    }
-    out[0] = c0;
-    out[1] = c1;
-    out[2] = c2;
-    out[3] = c3;
-}
-
-// G = -log(-log U) through the hardware base-2 logarithm (v_log_f32).
-// U = (floor(w / 2^9) + 1/2) 2^-23 takes 23 bits so that every value is an
-// exact fp32 number: it lies in [2^-24, 1 - 2^-24], never 0 or 1 (24 bits
-// would round the top value, 2^24 - 1/2, up to 2^24 and give U = 1, an
-// infinite score). -log U is then in [6.0e-8, 16.7], both ends normal, so no
-// range handling is needed; the log's error is below one ulp of the score.
-__device__ inline float gumbel(uint32_t w)
-{
-    constexpr float kLn2 = 0.693147180559945309f;
-    const float u = ((float)(w >> 9) + 0.5f) * (1.0f / 8388608.0f);
-    const float e = -kLn2 * __builtin_amdgcn_logf(u);
-    return -kLn2 * __builtin_amdgcn_logf(e);
-}
-
-// better(a, b): larger value, or the same value at a smaller index (selects,
-// no branches)
-__device__ inline void take_best(float &v, int &i, float v2, int i2)
-{
-    const bool b = (v2 > v) | ((v2 == v) & (i2 < i));
-    v = b ? v2 : v;
-    i = b ? i2 : i;
-}
-
-// merge of two log-sum-exp partials (either may be empty: z == 0)
-__device__ inline void merge_lse(float &m, float &z, float &s, float m2, float z2, float s2)
-{
-    if (z2 == 0.0f)
-        return;
-    if (z == 0.0f) {
-        m = m2;
-        z = z2;
-        s = s2;
-        return;
-    }
-    const float mm = fmaxf(m, m2);
-    const float a = __expf(m - mm), b = __expf(m2 - mm);
-    s = a * (s + (m - mm) * z) + b * (s2 + (m2 - mm) * z2);
-    z = a * z + b * z2;
-    m = mm;
-}
-
-__device__ inline void merge_partial(Partial &p, const Partial &q)
-{
-    merge_lse(p.m, p.z, p.s, q.m, q.z, q.s);
-    take_best(p.av, p.ai, q.av, q.ai);
-    take_best(p.sv, p.si, q.sv, q.si);
-}
 
 template <bool SMP>
 __global__ void __launch_bounds__(kSmpThreads) sample_partial_kernel(const f32x4v *__restrict__ logits,
