@@ -5,6 +5,7 @@
 #include "dgw4.h"
 
 #include "dgw4_internal.hpp"
+#include "step_end.hpp"
 
 #include <limits.h>
 

@@ -2,9 +2,7 @@
 // carries (not part of the ABI).
 #pragma once
 
-#include "dgw4_internal.hpp"
-
-#include "dgw4.h"
+#include "step_end.hpp"
 
 namespace dgw4 {
 namespace {

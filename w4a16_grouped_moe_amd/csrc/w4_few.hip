@@ -12,8 +12,7 @@
 // a group, lane (p, r) holds channel r's quarter p: its 16 (or 8) bytes are
 // two nibbles a byte in K order, eight nibbles a dword.
 #include "gemm_common.hpp"
-
-#include "dgw4.h"
+#include "step_end.hpp"
 
 namespace dgw4 {
 namespace {
