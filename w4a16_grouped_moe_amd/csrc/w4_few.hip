@@ -14,6 +14,8 @@
 #include "gemm_common.hpp"
 #include "step_end.hpp"
 
+#include <limits.h>
+
 namespace dgw4 {
 namespace {
 
@@ -56,73 +58,492 @@ __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 
 __device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
 
-// One wave: 16 channels, 16 tokens, all of K.
-template <class Tx, class Ty, int G>
-__global__ void __launch_bounds__(256) w4_few_kernel(W4FewArgs a)
+// How a call is cut up. A turn is what a workgroup takes at a time: its waves in
+// sets of 1 << split, each set 16 CB channels, the waves of a set every
+// (1 << split)-th group of K.
+struct Plan {
+    int split, turns, batches;
+    uint32_t magic;             // of the division by the vectors of a row (whole K in LDS)
+};
+
+// Groups of a batch: what a wave holds of the weights, each refilled with the
+// next batch's as soon as it has been used.
+template <int G>
+constexpr int kHeld = 512 / G;
+
+// Eight values of a token at column k8 * 8, at any alignment of the element.
+template <class Tx>
+__device__ inline uint4 get_x(const W4FewArgs &a, int t, int k8)
+{
+    uint4 v;
+    __builtin_memcpy(&v, (const Tx *)a.x + (size_t)t * a.ldx + k8 * 8, 16);
+    return v;
+}
+
+template <int CTRL>
+__device__ inline float dpp(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// The sum of a group's values, eight of them in each of G / 8 neighbouring lanes.
+template <class Tx, int G>
+__device__ inline float group_sum(uint4 v)
+{
+    const auto x = __builtin_bit_cast(typename Codes<Tx>::vec, v);
+    float s = (float)x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        s += (float)x[i];
+    s += dpp<0xB1>(s);                           // quad_perm: the neighbour
+    s += dpp<0x4E>(s);                           // quad_perm: the other pair
+    s += dpp<0x141>(s);                          // row_half_mirror: the other four of eight
+    if constexpr (G == 128)
+        s += dpp<0x140>(s);                      // row_mirror: the other eight of sixteen
+    return s;
+}
+
+// A wave's weights of 16 CB channels from n0 on, and where its lanes find them.
+template <int G, bool TL, int CB>
+struct Weights {
+    rsrc_t q, s, z;
+    int first, step;            // the groups of the batch: first, first + step, ...
+
+    __device__ Weights(const W4FewArgs &a, int n0, bool live, int first_, int step_) : first(first_), step(step_)
+    {
+        // in scalar registers, which the compiler does not see by itself
+        n0 = __builtin_amdgcn_readfirstlane(n0);
+        const int rows = __builtin_amdgcn_readfirstlane(live ? max(0, min(16 * CB, a.N - n0)) : 0);
+        const uint32_t groups = (uint32_t)a.K / G;
+        q = make_rsrc(a.q + (size_t)n0 * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
+        s = make_rsrc(a.s + (size_t)n0 * groups, (uint32_t)rows * groups * 2u);
+        z = make_rsrc(a.z + (size_t)n0 * groups, (uint32_t)rows * groups * 2u);
+    }
+};
+
+// The batch's group j of channel block c: past K or past the last channel, zeros.
+template <int G, bool TL, int CB>
+__device__ inline Frag<G> load_codes(const W4FewArgs &a, const Weights<G, TL, CB> &w, int c, int j, int lane)
+{
+    const int u = w.first + j * w.step, half = a.K / 2, r = lane & 15, p = lane >> 4;
+    const uint32_t past = u < a.K / G ? 0u : 0x80000000u;
+    const uint32_t at = TL ? (uint32_t)(c * 16 * half + lane * (G / 8)) + (uint32_t)u * (8u * G)
+                           : (uint32_t)((c * 16 + r) * half + p * (G / 8)) + (uint32_t)u * (G / 2u);
+    return load_frag<G, TL>(w.q, at | past, 0);
+}
+
+// Scale and zero point of channel r of block c in the batch's group j + p, in
+// one word: of four groups with one load each, a lane's quarter p saying which.
+template <int G, bool TL, int CB>
+__device__ inline uint32_t load_scales(const W4FewArgs &a, const Weights<G, TL, CB> &w, int c, int j, int lane)
+{
+    const int groups = a.K / G, u = w.first + (j + (lane >> 4)) * w.step;
+    const uint32_t at = u < groups ? (uint32_t)(((c * 16 + (lane & 15)) * groups + u) * 2) : 0x80000000u;
+    const uint32_t s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.s, at, 0, 0);
+    const uint32_t z = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.z, at, 0, 0);
+    return s | z << 16;
+}
+
+// The word of group j for all quarters.
+__device__ inline uint32_t spread(uint32_t v, int j, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(((j & 3) * 16 + (lane & 15)) * 4, (int)v);
+}
+
+// One group: its sums of 16 TB tokens by 16 CB channels, scaled, onto acc. x: the
+// lane's first vector of each token block in LDS; sums: the group's sums of x.
+template <class Tx, int G, int TB, int CB>
+__device__ inline void add_group(f32x4 (&acc)[TB][CB], const Frag<G> (&w)[CB], const uint32_t (&scales)[CB],
+                                 const char *const (&x)[TB], const float *sums, uint32_t base)
 {
     typedef typename Codes<Tx>::vec vec;
-    const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
-    const int item = blockIdx.x * 4 + ((int)threadIdx.x >> 6), t0 = blockIdx.y * 16;
-    if (item * 16 >= a.N)
-        return;
-    const int n = min(item * 16 + r, a.N - 1), groups = a.K / G;
-    const size_t row = (size_t)a.K / 2;
-    const uint8_t *q = a.tiled ? a.q + (size_t)item * 16 * row + lane * (G / 8) : a.q + (size_t)n * row + p * (G / 8);
-    const size_t step = a.tiled ? 8 * G : G / 2;
-    const Tx *x = (const Tx *)a.x + (size_t)min(t0 + r, a.T - 1) * a.ldx + p * (G / 4);
-    uint32_t base = Codes<Tx>::kBase;
-    asm("" : "+v"(base));
-    vec ones;
+    f32x4 sum[TB][CB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        ones[i] = (Tx)1.0f;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < groups; ++j) {
-        Frag<G> w = *reinterpret_cast<const Frag<G> *>(q + j * step);
-        const float s = half_bits(a.s[(size_t)n * groups + j]), z = half_bits(a.z[(size_t)n * groups + j]);
-        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f}, xs = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int i = 0; i < G / 32; ++i) {
-            uint4 v;
-            __builtin_memcpy(&v, x + j * G + i * 8, 16);
-            const vec xv = __builtin_bit_cast(vec, permute8(v));
-            sum = mfma(xv, codes8<Tx>(frag_word<G>(w, i), base), sum);
-            xs = mfma(xv, ones, xs);
+        for (int c = 0; c < CB; ++c)
+            sum[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < G / 32; ++i) {
+        vec q[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+            q[c] = codes8<Tx>(frag_word<G>(w[c], i), base);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const vec v = *reinterpret_cast<const vec *>(x[t] + i * 16);
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                sum[t][c] = mfma(v, q[c], sum[t][c]);
         }
-        acc += s * sum - s * (16.0f + z) * xs;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + p * 4 + i;
-        if (t < a.T && item * 16 + r < a.N)
-            ((Ty *)a.y)[(size_t)t * a.ldy + n] = (Ty)acc[i];
+    for (int c = 0; c < CB; ++c) {
+        const float s = half_bits((uint16_t)scales[c]);
+        const float sz = s * (16.0f + half_bits((uint16_t)(scales[c] >> 16)));
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            acc[t][c] += s * sum[t][c] - sz * *reinterpret_cast<const f32x4 *>(sums + t * 16);
     }
 }
 
-template <class Tx, class Ty>
-hipError_t run(const W4FewArgs &a, int g, hipStream_t st)
+// A turn's results from its waves' sums. With waves that share channels these
+// meet in LDS and are added in the waves' order.
+template <class Ty, int WAVES, int TB, int CB>
+__device__ inline void finish_as(const W4FewArgs &a, const Plan &pl, int turn, const f32x4 (&acc)[TB][CB],
+                                 f32x4 (*s_red)[CB][64])
 {
-    const dim3 grid((a.N + 63) / 64, (a.T + 15) / 16);
-    if (g == 128)
-        w4_few_kernel<Tx, Ty, 128><<<grid, dim3(256), 0, st>>>(a);
-    else
-        w4_few_kernel<Tx, Ty, 64><<<grid, dim3(256), 0, st>>>(a);
+    const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
+    const int wave = (int)threadIdx.x >> 6, sets = WAVES >> pl.split;
+    Ty *y = (Ty *)a.y;
+    if (pl.split == 0) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = t * 16 + p * 4 + i, n = ((turn * sets + wave) * CB + c) * 16 + r;
+                    if (tok < a.T && n < a.N)
+                        y[(size_t)tok * a.ldy + n] = (Ty)acc[t][c][i];
+                }
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        if (t * 16 >= a.T)
+            break;
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+            s_red[wave][c][lane] = acc[t][c];
+        __syncthreads();
+        // one output at a time per thread: token i, channel ch of a block
+        for (int o = threadIdx.x; o < sets * CB * 256; o += WAVES * 64) {
+            const int ch = o & 15, i = (o >> 4) & 15, c = (o >> 8) % CB, set = (o >> 8) / CB;
+            const int tok = t * 16 + i, n = ((turn * sets + set) * CB + c) * 16 + ch;
+            if (tok < a.T && n < a.N) {
+                float v = 0.0f;
+                for (int k = 0; k < 1 << pl.split; ++k)
+                    v += s_red[(set << pl.split) + k][c][(i >> 2) * 16 + ch][i & 3];
+                y[(size_t)tok * a.ldy + n] = (Ty)v;
+            }
+        }
+    }
+}
+
+template <int WAVES, int TB, int CB>
+__device__ inline void finish(const W4FewArgs &a, const Plan &pl, int turn, const f32x4 (&acc)[TB][CB],
+                              f32x4 (*s_red)[CB][64])
+{
+    switch (a.y_type) {
+    case DGW4_F32: finish_as<float, WAVES>(a, pl, turn, acc, s_red); break;
+    case DGW4_F16: finish_as<_Float16, WAVES>(a, pl, turn, acc, s_red); break;
+    default: finish_as<__bf16, WAVES>(a, pl, turn, acc, s_red);
+    }
+}
+
+// All activations in LDS, once: rows 16 bytes off the bank period, so that the 16
+// rows of a fragment fall on all banks.
+template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
+__global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Plan pl)
+{
+    constexpr int H = kHeld<G>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];     // [T][row], then [K/G][16 TB] sums
+    __shared__ f32x4 s_red[WAVES][CB][64];
+    const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int parts = 1 << pl.split, part = wave & (parts - 1), set = wave >> pl.split, sets = WAVES >> pl.split;
+    const int groups = a.K / G, row = a.K * 2 + 16;
+    float *sums = reinterpret_cast<float *>(lds + a.T * row);
+    uint32_t base = Codes<Tx>::kBase;
+    asm("" : "+v"(base));
+    auto source = [&](int turn, int b) {
+        const bool live = turn < pl.turns;
+        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H * parts + part, parts);
+    };
+
+    int turn = blockIdx.x;
+    Frag<G> w[H][CB];
+    uint32_t scales[H / 4][CB];
+    {
+        const auto q = source(turn, 0);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int j = 0; j < H / 4; ++j)
+                scales[j][c] = load_scales(a, q, c, j * 4, lane);
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                w[j][c] = load_codes(a, q, c, j, lane);
+        }
+    }
+    const int wide = a.K / 8;
+    for (int i = threadIdx.x; i < a.T * wide; i += WAVES * 64) {
+        const int t = (int)__umulhi((uint32_t)i, pl.magic), k8 = i - t * wide;
+        const uint4 v = get_x<Tx>(a, t, k8);
+        const float s = group_sum<Tx, G>(v);
+        *reinterpret_cast<uint4 *>(lds + t * row + k8 * 16) = permute8(v);
+        if (k8 % (G / 8) == 0)
+            sums[k8 / (G / 8) * (TB * 16) + t] = s;
+    }
+    __syncthreads();
+    const char *x0[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+        x0[t] = lds + min(t * 16 + r, a.T - 1) * row + p * (G / 2);
+    f32x4 acc[TB][CB];
+    for (int b = 0; turn < pl.turns;) {
+        const bool last = b == pl.batches - 1;
+        const int next_turn = last ? turn + (int)gridDim.x : turn, next_b = last ? 0 : b + 1;
+        const auto q = source(next_turn, next_b);
+        if (b == 0) {
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        uint32_t next[H / 4][CB];
+#pragma unroll
+        for (int j = 0; j < H / 4; ++j)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                next[j][c] = load_scales(a, q, c, j * 4, lane);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int u = (b * H + j) * parts + part;
+            if (u < groups) {
+                const char *x[TB];
+                uint32_t sc[CB];
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+                    x[t] = x0[t] + u * (G * 2);
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    sc[c] = spread(scales[j / 4][c], j, lane);
+                add_group<Tx, G>(acc, w[j], sc, x, sums + u * (TB * 16) + p * 4, base);
+            }
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                w[j][c] = load_codes(a, q, c, j, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < H / 4; ++j)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                scales[j][c] = next[j][c];
+        if (last)
+            finish<WAVES>(a, pl, turn, acc, s_red);
+        turn = next_turn;
+        b = next_b;
+    }
+}
+
+// The activations 512 columns at a time, in two halves of LDS: while one is
+// worked on, the next columns are on their way into registers.
+template <class Tx, int G, bool TL, int TB, int CB, int SPLIT>
+__global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArgs a, Plan pl)
+{
+    constexpr int H = kHeld<G>, WAVES = 8, kWide = 64, kRow = kWide * 16 + 16;
+    constexpr int parts = 1 << SPLIT, sets = WAVES >> SPLIT, kEach = H >> SPLIT;   // a wave's groups of a chunk
+    static_assert(kEach >= 1, "a wave has a group of each chunk");
+    extern __shared__ __attribute__((aligned(16))) char lds[];     // 2 x ([T][kRow], then [H][16 TB] sums)
+    __shared__ f32x4 s_red[WAVES][CB][64];
+    const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int part = wave & (parts - 1), set = wave >> SPLIT;
+    const int groups = a.K / G, bytes = a.T * kRow + H * TB * 64;
+    uint32_t base = Codes<Tx>::kBase;
+    asm("" : "+v"(base));
+    auto source = [&](int turn, int b) {
+        const bool live = turn < pl.turns;
+        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H * parts + part, parts);
+    };
+    // this thread's vectors of a chunk: row wave + 8 i, its lane's columns
+    uint4 held[TB * 2];
+    const int chunks = (groups + H - 1) / H;
+    auto fetch = [&](int chunk) {
+        const int k8 = min(chunk * kWide + lane, a.K / 8 - 1);      // past K: not met by a group
+#pragma unroll
+        for (int i = 0; i < TB * 2; ++i)
+            held[i] = get_x<Tx>(a, min(wave + 8 * i, a.T - 1), k8);
+    };
+    auto store = [&](char *at) {
+        float *sums = reinterpret_cast<float *>(at + a.T * kRow);
+#pragma unroll
+        for (int i = 0; i < TB * 2; ++i) {
+            const int t = wave + 8 * i;
+            if (t < a.T) {
+                const float s = group_sum<Tx, G>(held[i]);
+                *reinterpret_cast<uint4 *>(at + t * kRow + lane * 16) = permute8(held[i]);
+                if (lane % (G / 8) == 0)
+                    sums[lane / (G / 8) * (TB * 16) + t] = s;
+            }
+        }
+    };
+
+    int turn = blockIdx.x, chunk = 0, side = 0;
+    Frag<G> w[H][CB];
+    uint32_t scales[H / 4][CB];
+    fetch(0);
+    {
+        const auto q = source(turn, 0);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int j = 0; j < H / 4; ++j)
+                scales[j][c] = load_scales(a, q, c, j * 4, lane);
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                w[j][c] = load_codes(a, q, c, j, lane);
+        }
+    }
+    f32x4 acc[TB][CB];
+    for (int b = 0; turn < pl.turns;) {
+        const bool last = b == pl.batches - 1;
+        const int next_turn = last ? turn + (int)gridDim.x : turn, next_b = last ? 0 : b + 1;
+        const auto q = source(next_turn, next_b);
+        if (b == 0) {
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        uint32_t next[H / 4][CB];
+#pragma unroll
+        for (int j = 0; j < H / 4; ++j)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                next[j][c] = load_scales(a, q, c, j * 4, lane);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            if (j % kEach == 0 && b * parts + j / kEach < chunks) {
+                // the chunk's columns, which the loads have brought, into the half
+                // that was read last before the barrier before this one
+                side ^= 1;
+                store(lds + side * bytes);
+                chunk = chunk + 1 < chunks ? chunk + 1 : 0;
+                fetch(chunk);
+                __syncthreads();
+            }
+            const int u = (b * H + j) * parts + part;
+            if (u < groups) {
+                const char *half = lds + side * bytes;
+                const int at = (j % kEach) * parts + part;
+                const char *x[TB];
+                uint32_t sc[CB];
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+                    x[t] = half + min(t * 16 + r, a.T - 1) * kRow + p * (G / 2) + at * (G * 2);
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+                    sc[c] = spread(scales[j / 4][c], j, lane);
+                add_group<Tx, G>(acc, w[j], sc, x,
+                                 reinterpret_cast<const float *>(half + a.T * kRow) + at * (TB * 16) + p * 4, base);
+            }
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                w[j][c] = load_codes(a, q, c, j, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < H / 4; ++j)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                scales[j][c] = next[j][c];
+        if (last)
+            finish<WAVES>(a, pl, turn, acc, s_red);
+        turn = next_turn;
+        b = next_b;
+    }
+}
+
+constexpr size_t kLds = 160 * 1024;
+
+template <class Kern>
+hipError_t start(Kern kern, LdsAllowed &allowed, const W4FewArgs &a, const Plan &pl, size_t lds, int resident,
+                 int threads, hipStream_t st)
+{
+    const hipError_t err = allow_lds_here(kern, lds, allowed);
+    if (err != hipSuccess)
+        return err;
+    kern<<<dim3(pl.turns < resident ? pl.turns : resident), dim3(threads), lds, st>>>(a, pl);
     return hipGetLastError();
 }
 
-template <class Tx>
-hipError_t run_y(const W4FewArgs &a, int g, hipStream_t st)
+// The plan for `waves` waves a workgroup and `resident` workgroups on the chip
+// whose split takes the least time: rounds times groups a wave.
+Plan choose(const W4FewArgs &a, int groups, int held, int waves, int cb, int resident, int max_split)
 {
-    return a.y_type == DGW4_F32   ? run<Tx, float>(a, g, st)
-           : a.y_type == DGW4_F16 ? run<Tx, _Float16>(a, g, st)
-                                  : run<Tx, __bf16>(a, g, st);
+    Plan pl{};
+    long long best = LLONG_MAX;
+    for (int split = 0; split <= max_split; ++split) {
+        const int per = (waves >> split) * 16 * cb;
+        const long long turns = ((long long)a.N + per - 1) / per, rounds = (turns + resident - 1) / resident;
+        const long long each = (groups + (1 << split) - 1) >> split;
+        const long long cost = rounds * (each * 4 + (split ? 6 : 2));
+        if (cost < best) {
+            best = cost;
+            pl.split = split;
+            pl.turns = (int)turns;
+            pl.batches = (int)((each + held - 1) / held);
+        }
+    }
+    return pl;
+}
+
+template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
+hipError_t whole(const W4FewArgs &a, size_t lds, hipStream_t st)
+{
+    static LdsAllowed allowed;
+    const int resident = WAVES == 8 ? 512 : 256;
+    Plan pl = choose(a, a.K / G, kHeld<G>, WAVES, CB, resident, WAVES == 8 ? 3 : 4);
+    pl.magic = (uint32_t)(((1ull << 32) + a.K / 8 - 1) / (a.K / 8));
+    return start(w4_whole_kernel<Tx, G, TL, WAVES, TB, CB>, allowed, a, pl, lds, resident, WAVES * 64, st);
+}
+
+template <class Tx, int G, bool TL, int TB, int CB>
+hipError_t chunked(const W4FewArgs &a, hipStream_t st)
+{
+    static LdsAllowed allowed[3];
+    const size_t lds = 2 * ((size_t)a.T * (64 * 16 + 16) + kHeld<G> * TB * 64);
+    const int resident = TB == 1 && lds + 8 * CB * 1024 <= kLds / 2 ? 512 : 256;
+    const Plan pl = choose(a, a.K / G, kHeld<G>, 8, CB, resident, 2);
+    switch (pl.split) {
+    case 0: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 0>, allowed[0], a, pl, lds, resident, 512, st);
+    case 1: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 1>, allowed[1], a, pl, lds, resident, 512, st);
+    default: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 2>, allowed[2], a, pl, lds, resident, 512, st);
+    }
+}
+
+template <class Tx, int G, bool TL>
+hipError_t by_tokens(const W4FewArgs &a, hipStream_t st)
+{
+    if (a.T <= 16) {
+        const size_t lds = (size_t)a.T * (a.K * 2 + 16) + (size_t)(a.K / G) * 64;
+        if (lds + 8 * 1024 <= kLds / 2)
+            return whole<Tx, G, TL, 8, 1, 1>(a, lds, st);
+        if (lds + 16 * 1024 <= kLds)
+            return whole<Tx, G, TL, 16, 1, 1>(a, lds, st);
+        return chunked<Tx, G, TL, 1, 2>(a, st);
+    }
+    return a.T <= 32 ? chunked<Tx, G, TL, 2, 2>(a, st) : chunked<Tx, G, TL, 4, 2>(a, st);
+}
+
+template <class Tx>
+hipError_t by_layout(const W4FewArgs &a, int g, hipStream_t st)
+{
+    if (g == 128)
+        return a.tiled ? by_tokens<Tx, 128, true>(a, st) : by_tokens<Tx, 128, false>(a, st);
+    return a.tiled ? by_tokens<Tx, 64, true>(a, st) : by_tokens<Tx, 64, false>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_w4_few(const W4FewArgs &a, int g, hipStream_t stream)
 {
-    return a.x_type == DGW4_F16 ? run_y<_Float16>(a, g, stream) : run_y<__bf16>(a, g, stream);
+    return a.x_type == DGW4_F16 ? by_layout<_Float16>(a, g, stream) : by_layout<__bf16>(a, g, stream);
 }
 
 }  // namespace dgw4
