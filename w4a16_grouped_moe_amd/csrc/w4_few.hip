@@ -80,6 +80,18 @@ __device__ inline uint4 get_x(const W4FewArgs &a, int t, int k8)
     return v;
 }
 
+// The two values of a word onto s, exact products with one (subnormals count).
+template <class Tx>
+__device__ inline float pair_sum(uint32_t w, float s)
+{
+    typedef Tx pair __attribute__((ext_vector_type(2)));
+    const pair one = {(Tx)1.0f, (Tx)1.0f}, v = __builtin_bit_cast(pair, w);
+    if constexpr (Codes<Tx>::kTop == 6)
+        return __builtin_amdgcn_fdot2(v, one, s, false);
+    else
+        return __builtin_amdgcn_fdot2_f32_bf16(v, one, s, false);
+}
+
 template <int CTRL>
 __device__ inline float dpp(float v)
 {
@@ -90,11 +102,7 @@ __device__ inline float dpp(float v)
 template <class Tx, int G>
 __device__ inline float group_sum(uint4 v)
 {
-    const auto x = __builtin_bit_cast(typename Codes<Tx>::vec, v);
-    float s = (float)x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i)
-        s += (float)x[i];
+    float s = pair_sum<Tx>(v.y, pair_sum<Tx>(v.x, 0.0f)) + pair_sum<Tx>(v.w, pair_sum<Tx>(v.z, 0.0f));
     s += dpp<0xB1>(s);                           // quad_perm: the neighbour
     s += dpp<0x4E>(s);                           // quad_perm: the other pair
     s += dpp<0x141>(s);                          // row_half_mirror: the other four of eight
@@ -243,6 +251,8 @@ __device__ inline void finish(const W4FewArgs &a, const Plan &pl, int turn, cons
     }
 }
 
+constexpr int kAhead = 4;        // vectors of x a thread has on their way at once
+
 // All activations in LDS, once: rows 16 bytes off the bank period, so that the 16
 // rows of a fragment fall on all banks.
 template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
@@ -278,14 +288,27 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
                 w[j][c] = load_codes(a, q, c, j, lane);
         }
     }
-    const int wide = a.K / 8;
-    for (int i = threadIdx.x; i < a.T * wide; i += WAVES * 64) {
-        const int t = (int)__umulhi((uint32_t)i, pl.magic), k8 = i - t * wide;
-        const uint4 v = get_x<Tx>(a, t, k8);
-        const float s = group_sum<Tx, G>(v);
-        *reinterpret_cast<uint4 *>(lds + t * row + k8 * 16) = permute8(v);
-        if (k8 % (G / 8) == 0)
-            sums[k8 / (G / 8) * (TB * 16) + t] = s;
+    const int wide = a.K / 8, total = a.T * wide;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * WAVES * 64) {
+        uint4 v[kAhead];
+        int t[kAhead], k8[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * WAVES * 64;
+            t[j] = (int)__umulhi((uint32_t)i, pl.magic);
+            k8[j] = i - t[j] * wide;
+            if (i < total)
+                v[j] = get_x<Tx>(a, t[j], k8[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i0 + j * WAVES * 64 < total) {
+                const float s = group_sum<Tx, G>(v[j]);
+                *reinterpret_cast<uint4 *>(lds + t[j] * row + k8[j] * 16) = permute8(v[j]);
+                if (k8[j] % (G / 8) == 0)
+                    sums[k8[j] / (G / 8) * (TB * 16) + t[j]] = s;
+            }
+        }
     }
     __syncthreads();
     const char *x0[TB];
