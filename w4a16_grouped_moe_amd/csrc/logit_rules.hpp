@@ -8,8 +8,8 @@ namespace dgw4 {
 namespace {
 
 // A column's word: how often its token was generated in bits 0 .. 20, whether
-// the sequence holds it in bit 21, the place of its bias plus one above.
-constexpr uint32_t kCount = (1u << 21) - 1, kSeen = 1u << 21;
+// the prompt holds it in bit 21, the place of its bias plus one above.
+constexpr uint32_t kCount = (1u << 21) - 1, kPrompt = 1u << 21;
 constexpr int kPlaceBit = 22;
 
 // A sequence's rules.
@@ -58,7 +58,7 @@ __device__ inline float rounded_product(float a, float b)
 // l / 1, l - 0 * c, l - 0 and l * 1 are l (-0 - 0 is -0).
 __device__ inline float adjusted(float l, uint32_t word, const Sequence &q)
 {
-    if (word & kSeen)
+    if (word & (kPrompt | kCount))
         l = l > 0.0f ? l / q.repetition : rounded_product(l, q.repetition);
     const uint32_t c = word & kCount;
     if (c) {
@@ -67,7 +67,7 @@ __device__ inline float adjusted(float l, uint32_t word, const Sequence &q)
     }
     if (word >> kPlaceBit)
         l = l + q.bias[(word >> kPlaceBit) - 1];
-    return l * q.scale;
+    return rounded_product(l, q.scale);
 }
 
 }  // namespace
