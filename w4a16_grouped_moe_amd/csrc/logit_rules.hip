@@ -8,10 +8,9 @@
 // additions) go, whatever their order: no workspace, no sorting, and the rows
 // that share a sequence share the words. Each logit is read once.
 //
-// On their own the logits meet the words as they pass. Inside the sampler, where
-// the arithmetic counts, a wave first lists the few columns whose word is not
-// zero; the pass over its columns takes them like masked ones (one bit a column)
-// and the listed ones follow, a lane each.
+// The rules' arithmetic costs a lane about thirty instructions, and few columns
+// have a word: of each vector a lane takes one such column at a time, until no lane
+// of the wave has one left.
 //
 // A wave's part of a row (the maximum, its first place, sums of exp relative to
 // it, the best score) goes to the workspace; a second kernel joins a row's parts.
@@ -27,6 +26,7 @@ namespace dgw4 {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kJoin = 256;           // threads that join a row's parts
 
 // Columns of a workgroup's tile whose threads take E columns each, and of its waves.
 template <int E>
@@ -65,17 +65,37 @@ __device__ inline int across_min(int v)
     return across(v, [](int a, int b) { return min(a, b); });
 }
 
-// The words of columns c0 .. of sequence seq, by the whole workgroup.
+// The words of columns c0 .. of sequence seq, by the whole workgroup. The first
+// tokens are on their way while the words are cleared.
 template <int TILE>
 __device__ inline void enter(const dgw4_logit_rules &u, int seq, int c0, uint32_t *words)
 {
+    constexpr int kAhead = 4, kStep = kThreads * 4;  // loads of four tokens a thread has on their way
+    const int32_t *tok = u.tokens + (long long)max(seq, 0) * u.ld_tokens;
+    int n = 0, p = 0;
+    if (u.tokens && seq >= 0) {
+        n = min(max(u.lengths[seq], 0), u.max_tokens);
+        p = u.prompt_lengths ? u.prompt_lengths[seq] : 0;
+    }
+    int4 t[kAhead];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            t[j] = make_int4(-1, -1, -1, -1);
+            if (i0 + j * kStep + 3 < n)
+                __builtin_memcpy(&t[j], tok + i0 + j * kStep, 16);
+        }
+    };
+    int i0 = (int)threadIdx.x * 4;
+    load(i0);
+    // the last tokens, fewer than four
+    const int rest = (n & ~3) + (int)threadIdx.x;
+    const int last = rest < n ? tok[rest] : -1;
     __syncthreads();
-    for (int i = threadIdx.x * 4; i < TILE; i += kThreads * 4)
+    for (int i = threadIdx.x * 4; i < TILE; i += kStep)
         *reinterpret_cast<uint4 *>(words + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (seq < 0)
-        return;
-    if (u.n_bias > 0) {
+    if (u.n_bias > 0 && seq >= 0) {
         const int32_t *ids = u.bias_ids + (long long)seq * u.ld_bias;
         for (int j = threadIdx.x; j < u.n_bias; j += kThreads) {
             const uint32_t c = (uint32_t)ids[j] - (uint32_t)c0;
@@ -84,42 +104,29 @@ __device__ inline void enter(const dgw4_logit_rules &u, int seq, int c0, uint32_
         }
         __syncthreads();
     }
-    if (u.tokens) {
-        const int32_t *tok = u.tokens + (long long)seq * u.ld_tokens;
-        const int n = min(max(u.lengths[seq], 0), u.max_tokens);
-        const int p = u.prompt_lengths ? u.prompt_lengths[seq] : 0;
-        auto one = [&](int t, int i) {
-            const uint32_t c = (uint32_t)t - (uint32_t)c0;
-            if (c < (uint32_t)TILE) {
-                if (i < p)
-                    atomicOr(&words[c], kPrompt);
-                else
-                    atomicAdd(&words[c], 1u);
-            }
-        };
-        constexpr int kAhead = 4;                    // loads of four tokens a thread has on their way
-        int i = threadIdx.x * 4;
-        for (; i + (kAhead - 1) * kThreads * 4 + 3 < n; i += kAhead * kThreads * 4) {
-            int4 t[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                __builtin_memcpy(&t[j], tok + i + j * kThreads * 4, 16);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int at = i + j * kThreads * 4;
-                one(t[j].x, at);
-                one(t[j].y, at + 1);
-                one(t[j].z, at + 2);
-                one(t[j].w, at + 3);
-            }
+    // a token outside the tile, or none (-1), has no word
+    auto one = [&](int token, int i) {
+        const uint32_t c = (uint32_t)token - (uint32_t)c0;
+        if (c < (uint32_t)TILE) {
+            if (i < p)
+                atomicOr(&words[c], kPrompt);
+            else
+                atomicAdd(&words[c], 1u);
         }
-        for (; i < n; i += kThreads * 4)
+    };
+    for (; i0 < n; i0 += kAhead * kStep) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (i + k < n)
-                    one(tok[i + k], i + k);
-        __syncthreads();
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kStep;
+            one(t[j].x, i);
+            one(t[j].y, i + 1);
+            one(t[j].z, i + 2);
+            one(t[j].w, i + 3);
+        }
+        load(i0 + kAhead * kStep);
     }
+    one(last, rest);
+    __syncthreads();
 }
 
 // W neighbouring logits at any alignment of their element, read or written once.
@@ -150,6 +157,44 @@ __device__ inline uint32_t allowed(const uint32_t *mask, int c, int V)
     return mask && c < V ? mask[c >> 5] >> (c & 31) : ~0u;
 }
 
+// Which of a thread's columns have a word: bit k * W + i for column i of vector k,
+// whose words lie from words + k * step on.
+template <int W, int N>
+__device__ inline uint32_t with_words(const uint32_t *words, int step)
+{
+    uint32_t need = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            need |= words[k * step + i] != 0 ? 1u << (k * W + i) : 0u;
+    return need;
+}
+
+// A vector's logits after their sequence's rules; need: its columns with a word.
+template <int W>
+__device__ inline void follow_rules(float (&l)[W], uint32_t need, const uint32_t *words, const Sequence &q)
+{
+    float raw[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        raw[i] = l[i];
+        l[i] = rounded_product(l[i], q.scale);
+    }
+    while (__ballot(need != 0)) {
+        const int at = need ? __builtin_ctz(need) : W;
+        float v = raw[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i)
+            v = at == i ? raw[i] : v;
+        v = adjusted(v, words[at < W ? at : 0], q);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            l[i] = at == i ? v : l[i];
+        need &= need - 1;
+    }
+}
+
 // E columns a thread; SPARSE: in place and no scale, so only what changes is read and written.
 template <class Tx, class Ty, int E, bool HIST, bool SPARSE>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles, int rows)
@@ -158,50 +203,49 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile<E> : 4];
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile<E>;
+    const uint32_t *own = words + (HIST ? (int)threadIdx.x * W : 0);        // of this thread's first vector
+    constexpr uint32_t kAll = (1u << W) - 1;
     int seq = -2;
+    uint32_t needs = 0;
     for (int r = r0; r < min(r0 + rows, a.R); ++r) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
-        if (HIST && s != seq)
-            enter<kTile<E>>(a.rules, s, c0, words);
-        seq = s;
-        const Sequence q = sequence(a.rules, s);
         const Tx *row = (const Tx *)a.logits + (long long)r * a.ld;
         Ty *out = (Ty *)a.out + (long long)r * a.ld_out;
         typename Wide<Tx>::vec x[N];
-        uint32_t bits[N], any[N];
+        uint32_t bits[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
             bits[k] = allowed<W>(mask, c, a.V);
-            any[k] = 0;
-            if (HIST) {
-                const uint32_t *w = words + c - c0;
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    any[k] |= w[i];
-            }
-            if (c < a.V && (!SPARSE || any[k] || (bits[k] & ((1u << W) - 1)) != (1u << W) - 1))
+            if (!SPARSE && c < a.V)
                 x[k] = read_wide(row, c, a.V);
+        }
+        if (HIST && s != seq) {
+            enter<kTile<E>>(a.rules, s, c0, words);
+            needs = with_words<W, N>(own, kThreads * W);
+        }
+        seq = s;
+        const Sequence q = sequence(a.rules, s);
+        if (SPARSE) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
+                if (c < a.V && ((needs >> (k * W) & kAll) || (bits[k] & kAll) != kAll))
+                    x[k] = read_wide(row, c, a.V);
+            }
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
-            if (c >= a.V || (SPARSE && !any[k] && (bits[k] & ((1u << W) - 1)) == (1u << W) - 1))
-                continue;
+            const uint32_t need = c < a.V ? needs >> (k * W) & kAll : 0u;
             float l[W];
 #pragma unroll
             for (int i = 0; i < W; ++i)
                 l[i] = to_f32(x[k][i]);
-            if (HIST && any[k]) {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    l[i] = adjusted(l[i], words[c - c0 + i], q);
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    l[i] = rounded_product(l[i], q.scale);
-            }
+            follow_rules(l, need, own + k * kThreads * W, q);
+            if (c >= a.V || (SPARSE && !need && (bits[k] & kAll) == kAll))
+                continue;
             typedef Ty vec __attribute__((ext_vector_type(W), aligned(sizeof(Ty))));
             vec y;
 #pragma unroll
@@ -226,93 +270,54 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
 // it is zero also where d is infinite.
 __device__ inline float bounded(float d) { return fmaxf(d, -200.0f); }
 
-// A part of a row in a wave, the same in all lanes.
-struct Part {
-    float m, z, s;              // max, sum exp(l - m), sum exp(l - m) * (l - m)
-    int ai;                     // the first place of m
-    float sv;                   // the best score and its first place
-    int si;
-};
-
 template <class Tx, int E, bool HIST>
 __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W;
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile<E> : 4];
-    __shared__ uint32_t touched[HIST ? kTile<E> / 32 : 4];
-    __shared__ uint16_t listed[HIST ? kWaves : 1][HIST ? kPart<E> : 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile<E>, first = wave * kPart<E>;       // the tile's and, in it, the wave's columns
-    int seq = -2, count = 0;
+    const uint32_t *own = words + (HIST ? first + lane * W : 0);   // of this lane's first vector
+    int seq = -2;
+    uint32_t needs = 0;
     for (int r = r0; r < min(r0 + rows, a.R); ++r) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
         const Tx *row = (const Tx *)a.logits + (long long)r * a.ld;
-        const Sequence q = sequence(a.rules, s);
         typename Wide<Tx>::vec x[N];
+        uint32_t bits[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int c = c0 + first + (k * 64 + lane) * W;
             if (c < a.V)
                 x[k] = read_wide(row, c, a.V);
+            bits[k] = allowed<W>(mask, c, a.V);
+            if (c + W > a.V)
+                bits[k] &= c < a.V ? (1u << (a.V - c)) - 1 : 0u;
         }
         if (HIST && s != seq) {
             enter<kTile<E>>(a.rules, s, c0, words);
-            // the wave's columns with a word, in ascending order
-            count = 0;
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const bool is = words[first + k * 64 + lane] != 0;
-                const uint64_t all = __ballot(is);
-                if (lane == 0) {
-                    touched[(first + k * 64) / 32] = (uint32_t)all;
-                    touched[(first + k * 64) / 32 + 1] = (uint32_t)(all >> 32);
-                }
-                if (is)
-                    listed[wave][count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32),
-                                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] =
-                        (uint16_t)(first + k * 64 + lane);
-                count += __popcll(all);
-            }
-            // other lanes of the wave read them
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            needs = with_words<W, N>(own, 64 * W);
         }
         seq = s;
-        // the first of the listed, ahead of the columns' arithmetic
-        int lc = 0;
-        float ll = -INFINITY;
-        auto get_listed = [&](int at) {
-            ll = -INFINITY;
-            lc = INT_MAX;
-            if (at + lane < count) {
-                const int c = listed[wave][at + lane];
-                lc = c0 + c;
-                if (lc < a.V && (allowed<1>(mask, lc, a.V) & 1))
-                    ll = adjusted(to_f32(row[lc]), words[c], q);
-            }
-        };
-        if (HIST)
-            get_listed(0);
-
+        const Sequence q = sequence(a.rules, s);
         float l[E];
         float top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int c = c0 + first + (k * 64 + lane) * W;
-            uint32_t bits = allowed<W>(mask, c, a.V);
-            if (HIST)
-                bits &= ~(touched[(c - c0) >> 5] >> (c & 31));
-            if (c + W > a.V)
-                bits &= c < a.V ? (1u << (a.V - c)) - 1 : 0u;
+            float v[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                v[i] = to_f32(x[k][i]);
+            follow_rules(v, needs >> (k * W) & ((1u << W) - 1), own + k * 64 * W, q);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                l[k * W + i] = bits >> i & 1 ? rounded_product(to_f32(x[k][i]), q.scale) : -INFINITY;
+                l[k * W + i] = bits[k] >> i & 1 ? v[i] : -INFINITY;
                 top = fmaxf(top, l[k * W + i]);
             }
         }
-        Part p;
+        Partial p;
         p.m = across_max(top);
         const float m = p.m > -INFINITY ? p.m : 0.0f;
         p.z = p.m > -INFINITY ? 1.0f : 0.0f;
@@ -335,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs 
             for (int e = E - 1; e >= 0; --e)
                 at = l[e] == p.m ? (e / W * 64 + lane) * W + e % W : at;
         }
+        p.av = p.m;
         p.ai = across_min(at) + c0 + first;
         p.sv = -INFINITY;
         p.si = INT_MAX;
@@ -353,50 +359,27 @@ __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs 
                     best = g ? v : best;
                     where = g ? c + j : where;
                 }
+                __builtin_amdgcn_sched_barrier(0);   // one block at a time: its registers
             }
             p.sv = across_max(best);
             p.si = across_min(best == p.sv ? where : INT_MAX);
         }
-        for (int i = 0; HIST && i < count; i += 64) {
-            if (i > 0)
-                get_listed(i);
-            const float lm = across_max(ll);
-            if (!(lm > -INFINITY))
-                continue;
-            const int la = across_min(ll == lm ? lc : INT_MAX);
-            p.ai = lm > p.m ? la : lm == p.m ? min(la, p.ai) : p.ai;
-            const float nm = fmaxf(lm, p.m), d = bounded(p.m - nm), shrink = p.z > 0.0f ? __expf(d) : 0.0f;
-            const float ld = bounded(ll - nm), le = __expf(ld);
-            p.s = shrink * (p.s + d * p.z) + across_sum(le * ld);
-            p.z = shrink * p.z + across_sum(le);
-            p.m = nm;
-            if (a.sample) {
-                uint32_t w[4];
-                philox4x32_10((uint32_t)lc >> 2, (uint32_t)r, 0u, 0u, a.k0, a.k1, w);
-                const uint32_t word = lc & 2 ? lc & 1 ? w[3] : w[2] : lc & 1 ? w[1] : w[0];
-                const float v = ll + gumbel(word), best = across_max(v);
-                const int where = across_min(v == best ? lc : INT_MAX);
-                p.si = best > p.sv ? where : best == p.sv ? min(where, p.si) : p.si;
-                p.sv = fmaxf(best, p.sv);
-            }
-        }
-        if (lane == 0) {
-            const Partial out = {p.m, p.z, p.s, p.m, p.ai, p.sv, p.si, 0};
-            ((Partial *)a.parts)[((size_t)r * tiles + tile) * kWaves + wave] = out;
-        }
+        p.pad = 0;
+        if (lane == 0)
+            ((Partial *)a.parts)[((size_t)r * tiles + tile) * kWaves + wave] = p;
     }
 }
 
 // A workgroup for a row's parts: their maximum, then the sums relative to it.
-__global__ void __launch_bounds__(kThreads) join_kernel(LogitArgs a, int parts)
+__global__ void __launch_bounds__(kJoin) join_kernel(LogitArgs a, int parts)
 {
-    __shared__ float s_m[kWaves], s_v[kWaves], s_z[kWaves], s_s[kWaves];
-    __shared__ int s_a[kWaves], s_i[kWaves];
+    __shared__ float s_m[kJoin / 64], s_v[kJoin / 64], s_z[kJoin / 64], s_s[kJoin / 64];
+    __shared__ int s_a[kJoin / 64], s_i[kJoin / 64];
     const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     for (long long r = blockIdx.x; r < a.R; r += gridDim.x) {
         const Partial *part = (const Partial *)a.parts + (size_t)r * parts;
         float m = -INFINITY, v = -INFINITY;
-        for (int k = threadIdx.x; k < parts; k += kThreads) {
+        for (int k = threadIdx.x; k < parts; k += kJoin) {
             m = fmaxf(m, part[k].m);
             v = fmaxf(v, part[k].sv);
         }
@@ -412,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(LogitArgs a, int parts)
         const bool none = !(m > -INFINITY);
         float z = 0.0f, s = 0.0f;
         int ai = INT_MAX, si = INT_MAX;
-        for (int k = threadIdx.x; k < parts; k += kThreads) {
+        for (int k = threadIdx.x; k < parts; k += kJoin) {
             const Partial p = part[k];
             const float d = none ? 0.0f : bounded(p.m - m), e = __expf(d);
             z += e * p.z;
@@ -517,7 +500,7 @@ hipError_t sample(const LogitArgs &a, hipStream_t st)
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    join_kernel<<<dim3(a.R < (1 << 20) ? a.R : 1 << 20), dim3(kThreads), 0, st>>>(a, c.tiles * kWaves);
+    join_kernel<<<dim3(a.R < (1 << 20) ? a.R : 1 << 20), dim3(kJoin), 0, st>>>(a, c.tiles * kWaves);
     return hipGetLastError();
 }
 

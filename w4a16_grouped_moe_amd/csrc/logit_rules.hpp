@@ -58,13 +58,10 @@ __device__ inline float rounded_product(float a, float b)
 // l / 1, l - 0 * c, l - 0 and l * 1 are l (-0 - 0 is -0).
 __device__ inline float adjusted(float l, uint32_t word, const Sequence &q)
 {
-    if (word & (kPrompt | kCount))
-        l = l > 0.0f ? l / q.repetition : rounded_product(l, q.repetition);
     const uint32_t c = word & kCount;
-    if (c) {
-        l = l - rounded_product(q.frequency, (float)c);
-        l = l - q.presence;
-    }
+    const float penalised = l > 0.0f ? l / q.repetition : rounded_product(l, q.repetition);
+    const float less = penalised - rounded_product(q.frequency, (float)c);
+    l = c ? less - q.presence : word & kPrompt ? penalised : l;
     if (word >> kPlaceBit)
         l = l + q.bias[(word >> kPlaceBit) - 1];
     return rounded_product(l, q.scale);
