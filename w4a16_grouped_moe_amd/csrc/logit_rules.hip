@@ -9,8 +9,8 @@
 // that share a sequence share the words. Each logit is read once.
 //
 // The rules' arithmetic costs a lane about thirty instructions, and few columns
-// have a word: of each vector a lane takes one such column at a time, until no lane
-// of the wave has one left.
+// have a word: a lane takes one such column of its own at a time, until no lane of
+// the wave has one left.
 //
 // A wave's part of a row (the maximum, its first place, sums of exp relative to
 // it, the best score) goes to the workspace; a second kernel joins a row's parts.
@@ -86,7 +86,7 @@ __device__ inline void enter(const dgw4_logit_rules &u, int seq, int c0, uint32_
                 __builtin_memcpy(&t[j], tok + i0 + j * kStep, 16);
         }
     };
-    int i0 = (int)threadIdx.x * 4;
+    const int i0 = (int)threadIdx.x * 4;
     load(i0);
     // the last tokens, fewer than four
     const int rest = (n & ~3) + (int)threadIdx.x;
@@ -105,27 +105,44 @@ __device__ inline void enter(const dgw4_logit_rules &u, int seq, int c0, uint32_
         __syncthreads();
     }
     // a token outside the tile, or none (-1), has no word
-    auto one = [&](int token, int i) {
+    auto prompt = [&](int token) {
         const uint32_t c = (uint32_t)token - (uint32_t)c0;
-        if (c < (uint32_t)TILE) {
-            if (i < p)
-                atomicOr(&words[c], kPrompt);
-            else
-                atomicAdd(&words[c], 1u);
-        }
+        if (c < (uint32_t)TILE)
+            atomicOr(&words[c], kPrompt);
     };
-    for (; i0 < n; i0 += kAhead * kStep) {
+    auto generated = [&](int token) {
+        const uint32_t c = (uint32_t)token - (uint32_t)c0;
+        if (c < (uint32_t)TILE)
+            atomicAdd(&words[c], 1u);
+    };
+    auto either = [&](int token, int i) { i < p ? prompt(token) : generated(token); };
+    const int wave0 = __builtin_amdgcn_readfirstlane(i0);
+    for (int step = 0; wave0 + step < n; step += kAhead * kStep) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j * kStep;
-            one(t[j].x, i);
-            one(t[j].y, i + 1);
-            one(t[j].z, i + 2);
-            one(t[j].w, i + 3);
+            if (wave0 + step + j * kStep >= n)
+                break;
+            const int i = i0 + step + j * kStep;
+            if (i >= p) {
+                generated(t[j].x);
+                generated(t[j].y);
+                generated(t[j].z);
+                generated(t[j].w);
+            } else if (i + 3 < p) {
+                prompt(t[j].x);
+                prompt(t[j].y);
+                prompt(t[j].z);
+                prompt(t[j].w);
+            } else {
+                either(t[j].x, i);
+                either(t[j].y, i + 1);
+                either(t[j].z, i + 2);
+                either(t[j].w, i + 3);
+            }
         }
-        load(i0 + kAhead * kStep);
+        load(i0 + step + kAhead * kStep);
     }
-    one(last, rest);
+    either(last, rest);
     __syncthreads();
 }
 
@@ -150,6 +167,22 @@ __device__ inline typename Wide<T>::vec read_wide(const T *row, int c, int V)
     return v;
 }
 
+// A thread's N vectors, `step` columns apart from c on; inside: the tile ends before V does.
+template <class T, int N>
+__device__ inline void read_all(typename Wide<T>::vec (&x)[N], const T *row, int c, int step, int V, bool inside)
+{
+    typedef typename Wide<T>::vec vec;
+    if (inside) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            x[k] = __builtin_nontemporal_load(reinterpret_cast<const vec *>(row + c + k * step));
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            x[k] = read_wide(row, c + k * step, V);
+    }
+}
+
 // The mask's bits of columns c .. c + W - 1 (c a multiple of W) in the low bits; past V: anything.
 template <int W>
 __device__ inline uint32_t allowed(const uint32_t *mask, int c, int V)
@@ -167,32 +200,31 @@ __device__ inline uint32_t with_words(const uint32_t *words, int step)
     for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            need |= words[k * step + i] != 0 ? 1u << (k * W + i) : 0u;
+            need |= min(words[k * step + i], 1u) << (k * W + i);
     return need;
 }
 
-// A vector's logits after their sequence's rules; need: its columns with a word.
-template <int W>
-__device__ inline void follow_rules(float (&l)[W], uint32_t need, const uint32_t *words, const Sequence &q)
+// A thread's N vectors of W logits after their sequence's rules. need: the columns
+// with a word, as with_words() has them.
+template <int W, int N>
+__device__ inline void follow_rules(float (&l)[N * W], uint32_t need, const uint32_t *words, int step,
+                                    const Sequence &q)
 {
-    float raw[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        raw[i] = l[i];
-        l[i] = rounded_product(l[i], q.scale);
-    }
     while (__ballot(need != 0)) {
-        const int at = need ? __builtin_ctz(need) : W;
-        float v = raw[0];
+        const int at = need ? __builtin_ctz(need) : N * W;
+        float v = l[0];
 #pragma unroll
-        for (int i = 1; i < W; ++i)
-            v = at == i ? raw[i] : v;
-        v = adjusted(v, words[at < W ? at : 0], q);
+        for (int e = 1; e < N * W; ++e)
+            v = at == e ? l[e] : v;
+        v = adjusted(v, words[need ? at / W * step + at % W : 0], q);
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            l[i] = at == i ? v : l[i];
+        for (int e = 0; e < N * W; ++e)
+            l[e] = at == e ? v : l[e];
         need &= need - 1;
     }
+#pragma unroll
+    for (int e = 0; e < N * W; ++e)
+        l[e] = rounded_product(l[e], q.scale);
 }
 
 // E columns a thread; SPARSE: in place and no scale, so only what changes is read and written.
@@ -205,22 +237,22 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
     const int c0 = tile * kTile<E>;
     const uint32_t *own = words + (HIST ? (int)threadIdx.x * W : 0);        // of this thread's first vector
     constexpr uint32_t kAll = (1u << W) - 1;
+    const int mine = c0 + (int)threadIdx.x * W, end = min(r0 + rows, a.R);
+    const bool inside = c0 + kTile<E> <= a.V;
+    const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
+    Ty *out = (Ty *)a.out + (long long)r0 * a.ld_out;
+    typename Wide<Tx>::vec x[N];
+    if (!SPARSE)
+        read_all<Tx, N>(x, row, mine, kThreads * W, a.V, inside);
     int seq = -2;
     uint32_t needs = 0;
-    for (int r = r0; r < min(r0 + rows, a.R); ++r) {
+    for (int r = r0; r < end; ++r, row += a.ld, out += a.ld_out) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
-        const Tx *row = (const Tx *)a.logits + (long long)r * a.ld;
-        Ty *out = (Ty *)a.out + (long long)r * a.ld_out;
-        typename Wide<Tx>::vec x[N];
         uint32_t bits[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
-            bits[k] = allowed<W>(mask, c, a.V);
-            if (!SPARSE && c < a.V)
-                x[k] = read_wide(row, c, a.V);
-        }
+        for (int k = 0; k < N; ++k)
+            bits[k] = allowed<W>(mask, mine + k * kThreads * W, a.V);
         if (HIST && s != seq) {
             enter<kTile<E>>(a.rules, s, c0, words);
             needs = with_words<W, N>(own, kThreads * W);
@@ -230,27 +262,29 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
         if (SPARSE) {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
+                const int c = mine + k * kThreads * W;
                 if (c < a.V && ((needs >> (k * W) & kAll) || (bits[k] & kAll) != kAll))
                     x[k] = read_wide(row, c, a.V);
             }
         }
+        float l[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            l[e] = to_f32(x[e / W][e % W]);
+        // the next row's, behind this one's arithmetic
+        if (!SPARSE && r + 1 < end)
+            read_all<Tx, N>(x, row + a.ld, mine, kThreads * W, a.V, inside);
+        follow_rules<W, N>(l, needs, own, kThreads * W, q);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
-            const uint32_t need = c < a.V ? needs >> (k * W) & kAll : 0u;
-            float l[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                l[i] = to_f32(x[k][i]);
-            follow_rules(l, need, own + k * kThreads * W, q);
-            if (c >= a.V || (SPARSE && !need && (bits[k] & kAll) == kAll))
+            if (c >= a.V || (SPARSE && !(needs >> (k * W) & kAll) && (bits[k] & kAll) == kAll))
                 continue;
             typedef Ty vec __attribute__((ext_vector_type(W), aligned(sizeof(Ty))));
             vec y;
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                y[i] = from_f32<Ty>(bits[k] >> i & 1 ? l[i] : -INFINITY);
+                y[i] = from_f32<Ty>(bits[k] >> i & 1 ? l[k * W + i] : -INFINITY);
             if (c + W <= a.V) {
                 if constexpr (SPARSE)
                     *reinterpret_cast<vec *>(out + c) = y;
@@ -271,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
 __device__ inline float bounded(float d) { return fmaxf(d, -200.0f); }
 
 template <class Tx, int E, bool HIST>
-__global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
+__global__ void __launch_bounds__(kThreads, HIST ? 4 : 6) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W;
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile<E> : 4];
@@ -279,21 +313,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs 
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile<E>, first = wave * kPart<E>;       // the tile's and, in it, the wave's columns
     const uint32_t *own = words + (HIST ? first + lane * W : 0);   // of this lane's first vector
+    const int mine = c0 + first + lane * W, end = min(r0 + rows, a.R);
+    const bool inside = c0 + kTile<E> <= a.V;
+    const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
+    typename Wide<Tx>::vec x[N];
+    read_all<Tx, N>(x, row, mine, 64 * W, a.V, inside);
     int seq = -2;
     uint32_t needs = 0;
-    for (int r = r0; r < min(r0 + rows, a.R); ++r) {
+    for (int r = r0; r < end; ++r, row += a.ld) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
-        const Tx *row = (const Tx *)a.logits + (long long)r * a.ld;
-        typename Wide<Tx>::vec x[N];
         uint32_t bits[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const int c = c0 + first + (k * 64 + lane) * W;
-            if (c < a.V)
-                x[k] = read_wide(row, c, a.V);
+            const int c = mine + k * 64 * W;
             bits[k] = allowed<W>(mask, c, a.V);
-            if (c + W > a.V)
+            if (!inside && c + W > a.V)
                 bits[k] &= c < a.V ? (1u << (a.V - c)) - 1 : 0u;
         }
         if (HIST && s != seq) {
@@ -303,19 +338,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs 
         seq = s;
         const Sequence q = sequence(a.rules, s);
         float l[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            l[e] = to_f32(x[e / W][e % W]);
+        // the next row's, behind this one's arithmetic
+        if (r + 1 < end)
+            read_all<Tx, N>(x, row + a.ld, mine, 64 * W, a.V, inside);
+        follow_rules<W, N>(l, needs, own, 64 * W, q);
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float v[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                v[i] = to_f32(x[k][i]);
-            follow_rules(v, needs >> (k * W) & ((1u << W) - 1), own + k * 64 * W, q);
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                l[k * W + i] = bits[k] >> i & 1 ? v[i] : -INFINITY;
-                top = fmaxf(top, l[k * W + i]);
-            }
+        for (int e = 0; e < E; ++e) {
+            l[e] = bits[e / W] >> (e % W) & 1 ? l[e] : -INFINITY;
+            top = fmaxf(top, l[e]);
         }
         Partial p;
         p.m = across_max(top);
@@ -350,8 +384,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_adjusted_kernel(LogitArgs 
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
                 const int c = c0 + first + (e / W * 64 + lane) * W + e % W;
-                uint32_t w[4];
-                philox4x32_10((uint32_t)c >> 2, (uint32_t)r, 0u, 0u, a.k0, a.k1, w);
+                // (not known ahead of the rows: its first products would wait for
+                // them in registers)
+                uint32_t w[4], block = (uint32_t)c >> 2;
+                asm volatile("" : "+v"(block));
+                philox4x32_10(block, (uint32_t)r, 0u, 0u, a.k0, a.k1, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float v = l[e + j] + gumbel(w[j]);

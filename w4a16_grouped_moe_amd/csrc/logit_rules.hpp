@@ -54,8 +54,8 @@ __device__ inline float rounded_product(float a, float b)
     return v;
 }
 
-// A logit after its sequence's rules. An absent rule's constant changes no bits:
-// l / 1, l - 0 * c, l - 0 and l * 1 are l (-0 - 0 is -0).
+// A logit after its sequence's rules but the scale. An absent rule's constant
+// changes no bits: l / 1, l - 0 * c, l - 0 and, later, l * 1 are l (-0 - 0 is -0).
 __device__ inline float adjusted(float l, uint32_t word, const Sequence &q)
 {
     const uint32_t c = word & kCount;
@@ -64,7 +64,7 @@ __device__ inline float adjusted(float l, uint32_t word, const Sequence &q)
     l = c ? less - q.presence : word & kPrompt ? penalised : l;
     if (word >> kPlaceBit)
         l = l + q.bias[(word >> kPlaceBit) - 1];
-    return rounded_product(l, q.scale);
+    return l;
 }
 
 }  // namespace
