@@ -46,7 +46,7 @@ CASES = [
     (64, 6000, dict(L=20, S=2, scale=False)), (9, 515, dict(L=0, bias=12, penalties=False)),
     (6, 3000, dict(L=90, prompt=False, mask=True)), (3, 20000, dict(L=0, scale=False, mask=True)),
     (300, 1027, dict(L=33, S=7, bias=3, mask=True)), (5, 262144, dict(L=2000, mask=True, bias=9)),
-    (40, 70000, dict(L=400, S=5)), (130, 33000, dict(L=90, mask=True, S=130)),
+    (40, 70000, dict(L=400, S=5)), (130, 33000, dict(L=90, mask=True, S=130)), (64, 70001, dict(L=17000, bias=2, S=9)),
 ]
 
 

@@ -25,14 +25,18 @@
 namespace dgw4 {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+// Threads of a workgroup. Long histories take the wider one: each workgroup reads
+// its rows' whole histories, so half as many of them read half as much (64
+// sequences of 60000 tokens: 85 -> 71 us, one of 120000: 38 -> 25). Short ones
+// take the narrower: more workgroups on a compute unit hide each other's steps (a
+// canvas of 4 sequences of 8000: 85 us against 90).
+constexpr int kNarrow = 256, kBroad = 512;
+constexpr int kLongHistory = 16384;
 constexpr int kJoin = 256;           // threads that join a row's parts
 
-// Columns of a workgroup's tile whose threads take E columns each, and of its waves.
-template <int E>
-constexpr int kTile = kThreads * E;
-template <int E>
-constexpr int kPart = 64 * E;
+// Columns of a tile: of a workgroup of `threads` that take E columns each; of a wave.
+constexpr int tile_of(int threads, int e) { return threads * e; }
+constexpr int part_of(int e) { return 64 * e; }
 
 // v of all lanes joined: the lanes of a row of 16 by DPP, then the four rows.
 template <class T, class F>
@@ -67,7 +71,7 @@ __device__ inline int across_min(int v)
 
 // The words of columns c0 .. of sequence seq, by the whole workgroup. The first
 // tokens are on their way while the words are cleared.
-template <int TILE>
+template <int kThreads, int TILE>
 __device__ inline void enter(const dgw4_logit_rules &u, int seq, int c0, uint32_t *words)
 {
     constexpr int kAhead = 4, kStep = kThreads * 4;  // loads of four tokens a thread has on their way
@@ -228,17 +232,18 @@ __device__ inline void follow_rules(float (&l)[N * W], uint32_t need, const uint
 }
 
 // E columns a thread; SPARSE: in place and no scale, so only what changes is read and written.
-template <class Tx, class Ty, int E, bool HIST, bool SPARSE>
+template <class Tx, class Ty, int kThreads, int E, bool HIST, bool SPARSE>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W;        // columns of a vector, vectors of a thread
-    __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile<E> : 4];
+    constexpr int kTile = tile_of(kThreads, E);
+    __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile : 4];
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
-    const int c0 = tile * kTile<E>;
+    const int c0 = tile * kTile;
     const uint32_t *own = words + (HIST ? (int)threadIdx.x * W : 0);        // of this thread's first vector
     constexpr uint32_t kAll = (1u << W) - 1;
     const int mine = c0 + (int)threadIdx.x * W, end = min(r0 + rows, a.R);
-    const bool inside = c0 + kTile<E> <= a.V;
+    const bool inside = c0 + kTile <= a.V;
     const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
     Ty *out = (Ty *)a.out + (long long)r0 * a.ld_out;
     typename Wide<Tx>::vec x[N];
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
         for (int k = 0; k < N; ++k)
             bits[k] = allowed<W>(mask, mine + k * kThreads * W, a.V);
         if (HIST && s != seq) {
-            enter<kTile<E>>(a.rules, s, c0, words);
+            enter<kThreads, kTile>(a.rules, s, c0, words);
             needs = with_words<W, N>(own, kThreads * W);
         }
         seq = s;
@@ -304,17 +309,17 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
 // it is zero also where d is infinite.
 __device__ inline float bounded(float d) { return fmaxf(d, -200.0f); }
 
-template <class Tx, int E, bool HIST>
+template <class Tx, int kThreads, int E, bool HIST>
 __global__ void __launch_bounds__(kThreads, HIST ? 4 : 6) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
 {
-    constexpr int W = Wide<Tx>::W, N = E / W;
-    __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile<E> : 4];
+    constexpr int W = Wide<Tx>::W, N = E / W, kTile = tile_of(kThreads, E), kWaves = kThreads / 64;
+    __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile : 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
-    const int c0 = tile * kTile<E>, first = wave * kPart<E>;       // the tile's and, in it, the wave's columns
+    const int c0 = tile * kTile, first = wave * part_of(E);       // the tile's and, in it, the wave's columns
     const uint32_t *own = words + (HIST ? first + lane * W : 0);   // of this lane's first vector
     const int mine = c0 + first + lane * W, end = min(r0 + rows, a.R);
-    const bool inside = c0 + kTile<E> <= a.V;
+    const bool inside = c0 + kTile <= a.V;
     const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
     typename Wide<Tx>::vec x[N];
     read_all<Tx, N>(x, row, mine, 64 * W, a.V, inside);
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, HIST ? 4 : 6) sample_adjusted_kernel
                 bits[k] &= c < a.V ? (1u << (a.V - c)) - 1 : 0u;
         }
         if (HIST && s != seq) {
-            enter<kTile<E>>(a.rules, s, c0, words);
+            enter<kThreads, kTile>(a.rules, s, c0, words);
             needs = with_words<W, N>(own, 64 * W);
         }
         seq = s;
@@ -470,22 +475,22 @@ constexpr int kFew = 8, kMany = 16;
 
 int per_thread(int R, int V)
 {
-    return (long long)R * ((V + kPart<kMany> - 1) / kPart<kMany>) >= 4096 ? kMany : kFew;
+    return (long long)R * ((V + part_of(kMany) - 1) / part_of(kMany)) >= 4096 ? kMany : kFew;
 }
 
-// Tiles of a row, and the rows that a workgroup takes in turn: those of a
-// sequence lie next to each other where rows share sequences, and the words are
-// entered once for them.
+// Tiles of a row, and the rows that a workgroup takes in turn: where rows share
+// sequences, those of one lie next to each other, and the words are entered once
+// for them.
 struct Cut {
     int tiles, rows;
     uint32_t groups;
 };
 
-Cut cut(const LogitArgs &a, int e, bool shared)
+Cut cut(const LogitArgs &a, int tile, bool shared)
 {
     Cut c;
-    c.tiles = (a.V + kThreads * e - 1) / (kThreads * e);
-    const long long pairs = (long long)a.R * c.tiles, resident = 2048, most = 1 << 23;
+    c.tiles = (a.V + tile - 1) / tile;
+    const long long pairs = (long long)a.R * c.tiles, resident = 2048, most = 1 << 22;
     long long rows = shared ? (pairs + resident - 1) / resident : 1;
     rows = rows > 32 ? 32 : rows;
     if (pairs / rows > most)                         // a launch has at most 2^32 threads
@@ -496,55 +501,60 @@ Cut cut(const LogitArgs &a, int e, bool shared)
 }
 
 bool has_history(const dgw4_logit_rules &u) { return u.tokens || u.n_bias > 0; }
+bool has_long_history(const dgw4_logit_rules &u) { return u.tokens && u.max_tokens >= kLongHistory; }
 
-template <class Tx, class Ty, int E>
+template <class Tx, class Ty, int T, int E, bool HIST>
 hipError_t adjust(const LogitArgs &a, hipStream_t st)
 {
-    const bool hist = has_history(a.rules), sparse = a.logits == a.out && !a.rules.scale;
-    const Cut c = cut(a, E, hist && a.rules.row_seq);
-    const dim3 grid(c.groups), block(kThreads);
+    const Cut c = cut(a, tile_of(T, E), HIST && a.rules.row_seq);
     if constexpr (sizeof(Tx) == sizeof(Ty)) {
-        if (sparse) {
-            if (hist)
-                adjust_kernel<Tx, Ty, E, true, true><<<grid, block, 0, st>>>(a, c.tiles, c.rows);
-            else
-                adjust_kernel<Tx, Ty, E, false, true><<<grid, block, 0, st>>>(a, c.tiles, c.rows);
+        if (a.logits == a.out && !a.rules.scale) {
+            adjust_kernel<Tx, Ty, T, E, HIST, true><<<dim3(c.groups), dim3(T), 0, st>>>(a, c.tiles, c.rows);
             return hipGetLastError();
         }
     }
-    if (hist)
-        adjust_kernel<Tx, Ty, E, true, false><<<grid, block, 0, st>>>(a, c.tiles, c.rows);
-    else
-        adjust_kernel<Tx, Ty, E, false, false><<<grid, block, 0, st>>>(a, c.tiles, c.rows);
+    adjust_kernel<Tx, Ty, T, E, HIST, false><<<dim3(c.groups), dim3(T), 0, st>>>(a, c.tiles, c.rows);
     return hipGetLastError();
+}
+
+template <class Tx, class Ty, int E>
+hipError_t adjust_with(const LogitArgs &a, hipStream_t st)
+{
+    return !has_history(a.rules)       ? adjust<Tx, Ty, kNarrow, E, false>(a, st)
+           : has_long_history(a.rules) ? adjust<Tx, Ty, kBroad, E, true>(a, st)
+                                       : adjust<Tx, Ty, kNarrow, E, true>(a, st);
 }
 
 template <class Tx, class Ty>
 hipError_t adjust_sized(const LogitArgs &a, hipStream_t st)
 {
-    return per_thread(a.R, a.V) == kMany ? adjust<Tx, Ty, kMany>(a, st) : adjust<Tx, Ty, kFew>(a, st);
+    return per_thread(a.R, a.V) == kMany ? adjust_with<Tx, Ty, kMany>(a, st) : adjust_with<Tx, Ty, kFew>(a, st);
 }
 
-template <class Tx, int E>
+template <class Tx, int T, int E, bool HIST>
 hipError_t sample(const LogitArgs &a, hipStream_t st)
 {
-    const bool hist = has_history(a.rules);
-    const Cut c = cut(a, E, hist && a.rules.row_seq);
-    if (hist)
-        sample_adjusted_kernel<Tx, E, true><<<dim3(c.groups), dim3(kThreads), 0, st>>>(a, c.tiles, c.rows);
-    else
-        sample_adjusted_kernel<Tx, E, false><<<dim3(c.groups), dim3(kThreads), 0, st>>>(a, c.tiles, c.rows);
+    const Cut c = cut(a, tile_of(T, E), HIST && a.rules.row_seq);
+    sample_adjusted_kernel<Tx, T, E, HIST><<<dim3(c.groups), dim3(T), 0, st>>>(a, c.tiles, c.rows);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    join_kernel<<<dim3(a.R < (1 << 20) ? a.R : 1 << 20), dim3(kJoin), 0, st>>>(a, c.tiles * kWaves);
+    join_kernel<<<dim3(a.R < (1 << 20) ? a.R : 1 << 20), dim3(kJoin), 0, st>>>(a, c.tiles * (T / 64));
     return hipGetLastError();
+}
+
+template <class Tx, int E>
+hipError_t sample_with(const LogitArgs &a, hipStream_t st)
+{
+    return !has_history(a.rules)       ? sample<Tx, kNarrow, E, false>(a, st)
+           : has_long_history(a.rules) ? sample<Tx, kBroad, E, true>(a, st)
+                                       : sample<Tx, kNarrow, E, true>(a, st);
 }
 
 template <class Tx>
 hipError_t sample_sized(const LogitArgs &a, hipStream_t st)
 {
-    return per_thread(a.R, a.V) == kMany ? sample<Tx, kMany>(a, st) : sample<Tx, kFew>(a, st);
+    return per_thread(a.R, a.V) == kMany ? sample_with<Tx, kMany>(a, st) : sample_with<Tx, kFew>(a, st);
 }
 
 }  // namespace
@@ -562,10 +572,11 @@ hipError_t launch_adjust_logits(const LogitArgs &a, hipStream_t stream)
     }
 }
 
+// The parts of the rows at the wider workgroup, which has the more.
 size_t sample_adjusted_workspace_bytes(int R, int V)
 {
-    const int tile = kThreads * per_thread(R, V);
-    return (size_t)R * (size_t)((V + tile - 1) / tile) * kWaves * sizeof(Partial);
+    const int tile = tile_of(kBroad, per_thread(R, V));
+    return (size_t)R * (size_t)((V + tile - 1) / tile) * (kBroad / 64) * sizeof(Partial);
 }
 
 hipError_t launch_sample_adjusted(const LogitArgs &a, hipStream_t stream)
