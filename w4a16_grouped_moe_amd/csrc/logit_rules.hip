@@ -233,7 +233,7 @@ __device__ inline void follow_rules(float (&l)[N * W], uint32_t need, const uint
 
 // E columns a thread; SPARSE: in place and no scale, so only what changes is read and written.
 template <class Tx, class Ty, int kThreads, int E, bool HIST, bool SPARSE>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles, int rows)
+__global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W;        // columns of a vector, vectors of a thread
     constexpr int kTile = tile_of(kThreads, E);
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(LogitArgs a, int tiles
 __device__ inline float bounded(float d) { return fmaxf(d, -200.0f); }
 
 template <class Tx, int kThreads, int E, bool HIST>
-__global__ void __launch_bounds__(kThreads, HIST ? 4 : 6) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
+__global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W, kTile = tile_of(kThreads, E), kWaves = kThreads / 64;
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile : 4];
