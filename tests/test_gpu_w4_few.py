@@ -47,7 +47,8 @@ def _check(y, x, w, g):
 SHAPES = [(1, 64, 1), (1, 128, 16), (2, 192, 5), (3, 704, 2111), (1, 2816, 300), (5, 2816, 1030), (7, 64, 4097),
           (8, 128, 20000), (15, 1088, 33), (16, 4096, 256), (17, 256, 100), (31, 2816, 47), (33, 960, 1000),
           (47, 128, 16400), (48, 8192, 40), (49, 1152, 255), (64, 2816, 513), (64, 64, 15), (64, 16384, 16),
-          (4, 28672, 20), (1, 100096, 3), (20, 40960, 18), (12, 5632, 2000)]
+          (4, 28672, 20), (1, 100096, 3), (20, 40960, 18), (12, 5632, 2000),
+          (3, 35264, 50), (16, 8256, 33), (9, 12352, 9000), (64, 4160, 5000), (30, 3008, 9000), (16, 6400, 40000)]
 
 
 @pytest.mark.parametrize("xt", [F16, BF16], ids=str)

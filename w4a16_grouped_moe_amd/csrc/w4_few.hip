@@ -60,7 +60,7 @@ __device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast
 
 // How a call is cut up. A turn is what a workgroup takes at a time: its waves in
 // sets of 1 << split, each set 16 CB channels, the waves of a set every
-// (1 << split)-th group of K.
+// (1 << split)-th 128 columns of K.
 struct Plan {
     int split, turns, batches;
     uint32_t magic;             // of the division by the vectors of a row (whole K in LDS)
@@ -70,6 +70,27 @@ struct Plan {
 // next batch's as soon as it has been used.
 template <int G>
 constexpr int kHeld = 512 / G;
+
+// Groups of 64 go in pairs: 128 columns are a wave's unit in any case.
+template <int G>
+constexpr int kPair = 128 / G;
+
+// The group of K that is a wave's i-th, as one of 1 << split waves.
+template <int G>
+__device__ inline int group_of(int i, int parts, int part)
+{
+    return i / kPair<G> * kPair<G> * parts + part * kPair<G> + i % kPair<G>;
+}
+
+// The quarter of a group that a lane holds: its own, or, in groups of 64, the one
+// that row-major weights leave it after their exchange (see load_codes), in both
+// layouts, whose results then have the same bits.
+template <int G>
+__device__ inline int quarter(int lane)
+{
+    const int p = lane >> 4;
+    return G == 64 ? (p & 1) * 2 + (p >> 1) : p;
+}
 
 // Eight values of a token at column k8 * 8, at any alignment of the element.
 template <class Tx>
@@ -111,13 +132,14 @@ __device__ inline float group_sum(uint4 v)
     return s;
 }
 
-// A wave's weights of 16 CB channels from n0 on, and where its lanes find them.
+// A wave's weights of 16 CB channels from n0 on, and which of its groups a batch begins with.
 template <int G, bool TL, int CB>
 struct Weights {
     rsrc_t q, s, z;
-    int first, step;            // the groups of the batch: first, first + step, ...
+    int first, parts, part;     // groups group_of(first + j, parts, part)
 
-    __device__ Weights(const W4FewArgs &a, int n0, bool live, int first_, int step_) : first(first_), step(step_)
+    __device__ Weights(const W4FewArgs &a, int n0, bool live, int first_, int parts_, int part_)
+        : first(first_), parts(parts_), part(part_)
     {
         // in scalar registers, which the compiler does not see by itself
         n0 = __builtin_amdgcn_readfirstlane(n0);
@@ -129,15 +151,56 @@ struct Weights {
     }
 };
 
-// The batch's group j of channel block c: past K or past the last channel, zeros.
-template <int G, bool TL, int CB>
-__device__ inline Frag<G> load_codes(const W4FewArgs &a, const Weights<G, TL, CB> &w, int c, int j, int lane)
+// The batch's groups j .. j + kPair - 1 of channel block c: past K or past the last
+// channel, zeros. Row-major groups of 64 have 32 bytes a row; a lane reads 16 of
+// the pair's 64, so that a row's lanes read them in one piece, and the lanes of
+// the two groups exchange halves when they are used (paired()).
+template <int G, bool TL, int CB, int H>
+__device__ inline void load_codes(const W4FewArgs &a, const Weights<G, TL, CB> &w, Frag<G> (&to)[H][CB], int c, int j,
+                                  int lane)
 {
-    const int u = w.first + j * w.step, half = a.K / 2, r = lane & 15, p = lane >> 4;
-    const uint32_t past = u < a.K / G ? 0u : 0x80000000u;
-    const uint32_t at = TL ? (uint32_t)(c * 16 * half + lane * (G / 8)) + (uint32_t)u * (8u * G)
-                           : (uint32_t)((c * 16 + r) * half + p * (G / 8)) + (uint32_t)u * (G / 2u);
-    return load_frag<G, TL>(w.q, at | past, 0);
+    const int u = group_of<G>(w.first + j, w.parts, w.part), groups = a.K / G;
+    const int half = a.K / 2, r = lane & 15, p = lane >> 4;
+    if constexpr (G == 64 && !TL) {
+        const uint32_t past = u + (p >> 1) < groups ? 0u : 0x80000000u;
+        const uint32_t at = (uint32_t)((c * 16 + r) * half + p * 16) + (uint32_t)u * (G / 2u);
+        const uint4 v = load16(w.q, at | past, 0);
+        to[j][c].v = make_uint2(v.x, v.y);
+        to[j + 1][c].v = make_uint2(v.z, v.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPair<G>; ++i) {
+            const uint32_t past = u + i < groups ? 0u : 0x80000000u;
+            const uint32_t at = TL ? (uint32_t)(c * 16 * half + (quarter<G>(lane) * 16 + r) * (G / 8)) +
+                                         (uint32_t)(u + i) * (8u * G)
+                                   : (uint32_t)((c * 16 + r) * half + p * (G / 8)) + (uint32_t)(u + i) * (G / 2u);
+            to[j + i][c] = load_frag<G, TL>(w.q, at | past, 0);
+        }
+    }
+}
+
+// Two row-major groups of 64 as they were loaded: lanes 0 .. 31 hold the first's 32
+// bytes of each row, lanes 32 .. 63 the second's. The upper lanes' first halves
+// against the lower lanes' second ones, and each register is of one group.
+__device__ inline void paired(Frag<64> &a, Frag<64> &b)
+{
+    const auto x = __builtin_amdgcn_permlane32_swap(a.v.x, b.v.x, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a.v.y, b.v.y, false, false);
+    a.v = make_uint2(x[0], y[0]);
+    b.v = make_uint2(x[1], y[1]);
+}
+
+// The same for the groups j and j + 1 of a batch, where they are such.
+template <int G, bool TL, int H, int CB>
+__device__ inline void pair_up(Frag<G> (&w)[H][CB], int j)
+{
+    if constexpr (G == 64 && !TL) {
+        if (j % 2 == 0) {
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                paired(w[j][c], w[j + 1][c]);
+        }
+    }
 }
 
 // Scale and zero point of channel r of block c in the batch's group j + p, in
@@ -145,7 +208,7 @@ __device__ inline Frag<G> load_codes(const W4FewArgs &a, const Weights<G, TL, CB
 template <int G, bool TL, int CB>
 __device__ inline uint32_t load_scales(const W4FewArgs &a, const Weights<G, TL, CB> &w, int c, int j, int lane)
 {
-    const int groups = a.K / G, u = w.first + (j + (lane >> 4)) * w.step;
+    const int groups = a.K / G, u = group_of<G>(w.first + j + (lane >> 4), w.parts, w.part);
     const uint32_t at = u < groups ? (uint32_t)(((c * 16 + (lane & 15)) * groups + u) * 2) : 0x80000000u;
     const uint32_t s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.s, at, 0, 0);
     const uint32_t z = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.z, at, 0, 0);
@@ -196,15 +259,15 @@ __device__ inline void add_group(f32x4 (&acc)[TB][CB], const Frag<G> (&w)[CB], c
 }
 
 // A turn's results from its waves' sums. With waves that share channels these
-// meet in LDS and are added in the waves' order.
-template <class Ty, int WAVES, int TB, int CB>
-__device__ inline void finish_as(const W4FewArgs &a, const Plan &pl, int turn, const f32x4 (&acc)[TB][CB],
-                                 f32x4 (*s_red)[CB][64])
+// meet in LDS, AT token blocks at a time, and are added in the waves' order.
+template <class Ty, int WAVES, int AT, int TB, int CB>
+__device__ inline void finish_as(const W4FewArgs &a, int split, int turn, const f32x4 (&acc)[TB][CB],
+                                 f32x4 (*s_red)[AT][CB][64])
 {
     const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
-    const int wave = (int)threadIdx.x >> 6, sets = WAVES >> pl.split;
+    const int wave = (int)threadIdx.x >> 6, sets = WAVES >> split;
     Ty *y = (Ty *)a.y;
-    if (pl.split == 0) {
+    if (split == 0) {
 #pragma unroll
         for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -218,40 +281,40 @@ __device__ inline void finish_as(const W4FewArgs &a, const Plan &pl, int turn, c
         return;
     }
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        if (t * 16 >= a.T)
-            break;
+    for (int t0 = 0; t0 < TB; t0 += AT) {
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
-            s_red[wave][c][lane] = acc[t][c];
+        for (int t = 0; t < AT; ++t)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+                s_red[wave][t][c][lane] = acc[t0 + t][c];
         __syncthreads();
-        // one output at a time per thread: token i, channel ch of a block
-        for (int o = threadIdx.x; o < sets * CB * 256; o += WAVES * 64) {
-            const int ch = o & 15, i = (o >> 4) & 15, c = (o >> 8) % CB, set = (o >> 8) / CB;
-            const int tok = t * 16 + i, n = ((turn * sets + set) * CB + c) * 16 + ch;
+        // one output at a time per thread: token i of a block, channel ch of a block
+        for (int o = threadIdx.x; o < AT * sets * CB * 256; o += WAVES * 64) {
+            const int ch = o & 15, i = (o >> 4) & 15, c = (o >> 8) % CB, set = (o >> 8) / CB % sets;
+            const int t = (o >> 8) / CB / sets, tok = (t0 + t) * 16 + i;
+            const int n = ((turn * sets + set) * CB + c) * 16 + ch;
             if (tok < a.T && n < a.N) {
                 float v = 0.0f;
-                for (int k = 0; k < 1 << pl.split; ++k)
-                    v += s_red[(set << pl.split) + k][c][(i >> 2) * 16 + ch][i & 3];
+                for (int k = 0; k < 1 << split; ++k)
+                    v += s_red[(set << split) + k][t][c][(i >> 2) * 16 + ch][i & 3];
                 y[(size_t)tok * a.ldy + n] = (Ty)v;
             }
         }
     }
+    __syncthreads();
 }
 
-template <int WAVES, int TB, int CB>
-__device__ inline void finish(const W4FewArgs &a, const Plan &pl, int turn, const f32x4 (&acc)[TB][CB],
-                              f32x4 (*s_red)[CB][64])
+template <int WAVES, int AT, int TB, int CB>
+__device__ inline void finish(const W4FewArgs &a, int split, int turn, const f32x4 (&acc)[TB][CB],
+                              f32x4 (*s_red)[AT][CB][64])
 {
     switch (a.y_type) {
-    case DGW4_F32: finish_as<float, WAVES>(a, pl, turn, acc, s_red); break;
-    case DGW4_F16: finish_as<_Float16, WAVES>(a, pl, turn, acc, s_red); break;
-    default: finish_as<__bf16, WAVES>(a, pl, turn, acc, s_red);
+    case DGW4_F32: finish_as<float, WAVES>(a, split, turn, acc, s_red); break;
+    case DGW4_F16: finish_as<_Float16, WAVES>(a, split, turn, acc, s_red); break;
+    default: finish_as<__bf16, WAVES>(a, split, turn, acc, s_red);
     }
 }
-
-constexpr int kAhead = 4;        // vectors of x a thread has on their way at once
 
 // All activations in LDS, once: rows 16 bytes off the bank period, so that the 16
 // rows of a fragment fall on all banks.
@@ -260,7 +323,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
 {
     constexpr int H = kHeld<G>;
     extern __shared__ __attribute__((aligned(16))) char lds[];     // [T][row], then [K/G][16 TB] sums
-    __shared__ f32x4 s_red[WAVES][CB][64];
+    __shared__ f32x4 s_red[WAVES][1][CB][64];
     const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int parts = 1 << pl.split, part = wave & (parts - 1), set = wave >> pl.split, sets = WAVES >> pl.split;
@@ -270,7 +333,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
     asm("" : "+v"(base));
     auto source = [&](int turn, int b) {
         const bool live = turn < pl.turns;
-        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H * parts + part, parts);
+        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H, parts, part);
     };
 
     int turn = blockIdx.x;
@@ -284,10 +347,11 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
             for (int j = 0; j < H / 4; ++j)
                 scales[j][c] = load_scales(a, q, c, j * 4, lane);
 #pragma unroll
-            for (int j = 0; j < H; ++j)
-                w[j][c] = load_codes(a, q, c, j, lane);
+            for (int j = 0; j < H; j += kPair<G>)
+                load_codes(a, q, w, c, j, lane);
         }
     }
+    constexpr int kAhead = WAVES == 16 ? 8 : 4;      // vectors of x a thread has on their way at once
     const int wide = a.K / 8, total = a.T * wide;
     for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * WAVES * 64) {
         uint4 v[kAhead];
@@ -314,7 +378,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
     const char *x0[TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t)
-        x0[t] = lds + min(t * 16 + r, a.T - 1) * row + p * (G / 2);
+        x0[t] = lds + min(t * 16 + r, a.T - 1) * row + quarter<G>(lane) * (G / 2);
     f32x4 acc[TB][CB];
     for (int b = 0; turn < pl.turns;) {
         const bool last = b == pl.batches - 1;
@@ -335,7 +399,8 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
                 next[j][c] = load_scales(a, q, c, j * 4, lane);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            const int u = (b * H + j) * parts + part;
+            const int u = group_of<G>(b * H + j, parts, part);
+            pair_up<G, TL>(w, j);
             if (u < groups) {
                 const char *x[TB];
                 uint32_t sc[CB];
@@ -347,9 +412,11 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
                     sc[c] = spread(scales[j / 4][c], j, lane);
                 add_group<Tx, G>(acc, w[j], sc, x, sums + u * (TB * 16) + p * 4, base);
             }
+            if (j % kPair<G> == kPair<G> - 1) {
 #pragma unroll
-            for (int c = 0; c < CB; ++c)
-                w[j][c] = load_codes(a, q, c, j, lane);
+                for (int c = 0; c < CB; ++c)
+                    load_codes(a, q, w, c, j - j % kPair<G>, lane);
+            }
         }
 #pragma unroll
         for (int j = 0; j < H / 4; ++j)
@@ -357,51 +424,53 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
             for (int c = 0; c < CB; ++c)
                 scales[j][c] = next[j][c];
         if (last)
-            finish<WAVES>(a, pl, turn, acc, s_red);
+            finish<WAVES>(a, pl.split, turn, acc, s_red);
         turn = next_turn;
         b = next_b;
     }
 }
 
-// The activations 512 columns at a time, in two halves of LDS: while one is
+// The activations M x 512 columns at a time, in two halves of LDS: while one is
 // worked on, the next columns are on their way into registers.
-template <class Tx, int G, bool TL, int TB, int CB, int SPLIT>
-__global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArgs a, Plan pl)
+template <class Tx, int G, bool TL, int WAVES, int TB, int CB, int M, int SPLIT>
+__global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kernel(W4FewArgs a, Plan pl)
 {
-    constexpr int H = kHeld<G>, WAVES = 8, kWide = 64, kRow = kWide * 16 + 16;
-    constexpr int parts = 1 << SPLIT, sets = WAVES >> SPLIT, kEach = H >> SPLIT;   // a wave's groups of a chunk
-    static_assert(kEach >= 1, "a wave has a group of each chunk");
-    extern __shared__ __attribute__((aligned(16))) char lds[];     // 2 x ([T][kRow], then [H][16 TB] sums)
-    __shared__ f32x4 s_red[WAVES][CB][64];
+    constexpr int H = kHeld<G>, kWide = 64 * M, kRow = kWide * 16 + 16, kMine = TB * 16 * M / WAVES;
+    constexpr int parts = 1 << SPLIT, sets = WAVES >> SPLIT, kEach = H * M >> SPLIT;   // a wave's groups of a chunk
+    static_assert(kEach >= kPair<G>, "a wave has 128 columns of each chunk");
+    extern __shared__ __attribute__((aligned(16))) char lds[];     // 2 x ([T][kRow], then [H M][16 TB] sums)
     const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int part = wave & (parts - 1), set = wave >> SPLIT;
-    const int groups = a.K / G, bytes = a.T * kRow + H * TB * 64;
+    const int groups = a.K / G, bytes = a.T * kRow + H * M * TB * 64;
     uint32_t base = Codes<Tx>::kBase;
     asm("" : "+v"(base));
     auto source = [&](int turn, int b) {
         const bool live = turn < pl.turns;
-        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H * parts + part, parts);
+        return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H, parts, part);
     };
-    // this thread's vectors of a chunk: row wave + 8 i, its lane's columns
-    uint4 held[TB * 2];
-    const int chunks = (groups + H - 1) / H;
+    // this thread's vectors of a chunk: 64 neighbouring ones of a row per wave
+    uint4 held[kMine];
+    const int chunks = (groups + H * M - 1) / (H * M);
+    auto row_of = [&](int i) { return (i * WAVES + wave) / M; };
+    const int mine = wave % M * 64 + lane;           // its column of vectors, the same in each row: M divides WAVES
     auto fetch = [&](int chunk) {
-        const int k8 = min(chunk * kWide + lane, a.K / 8 - 1);      // past K: not met by a group
+        const int k8 = min(chunk * kWide + mine, a.K / 8 - 1);      // past K: not met by a group
 #pragma unroll
-        for (int i = 0; i < TB * 2; ++i)
-            held[i] = get_x<Tx>(a, min(wave + 8 * i, a.T - 1), k8);
+        for (int i = 0; i < kMine; ++i)
+            if (row_of(i) < a.T)
+                held[i] = get_x<Tx>(a, row_of(i), k8);
     };
     auto store = [&](char *at) {
         float *sums = reinterpret_cast<float *>(at + a.T * kRow);
 #pragma unroll
-        for (int i = 0; i < TB * 2; ++i) {
-            const int t = wave + 8 * i;
+        for (int i = 0; i < kMine; ++i) {
+            const int t = row_of(i);
             if (t < a.T) {
                 const float s = group_sum<Tx, G>(held[i]);
-                *reinterpret_cast<uint4 *>(at + t * kRow + lane * 16) = permute8(held[i]);
+                *reinterpret_cast<uint4 *>(at + t * kRow + mine * 16) = permute8(held[i]);
                 if (lane % (G / 8) == 0)
-                    sums[lane / (G / 8) * (TB * 16) + t] = s;
+                    sums[mine / (G / 8) * (TB * 16) + t] = s;
             }
         }
     };
@@ -418,8 +487,8 @@ __global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArg
             for (int j = 0; j < H / 4; ++j)
                 scales[j][c] = load_scales(a, q, c, j * 4, lane);
 #pragma unroll
-            for (int j = 0; j < H; ++j)
-                w[j][c] = load_codes(a, q, c, j, lane);
+            for (int j = 0; j < H; j += kPair<G>)
+                load_codes(a, q, w, c, j, lane);
         }
     }
     f32x4 acc[TB][CB];
@@ -442,7 +511,8 @@ __global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArg
                 next[j][c] = load_scales(a, q, c, j * 4, lane);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            if (j % kEach == 0 && b * parts + j / kEach < chunks) {
+            const int i = b * H + j;
+            if (i % kEach == 0 && i / kEach < chunks) {
                 // the chunk's columns, which the loads have brought, into the half
                 // that was read last before the barrier before this one
                 side ^= 1;
@@ -451,24 +521,27 @@ __global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArg
                 fetch(chunk);
                 __syncthreads();
             }
-            const int u = (b * H + j) * parts + part;
+            const int u = group_of<G>(i, parts, part);
+            pair_up<G, TL>(w, j);
             if (u < groups) {
                 const char *half = lds + side * bytes;
-                const int at = (j % kEach) * parts + part;
+                const int at = group_of<G>(i % kEach, parts, part);
                 const char *x[TB];
                 uint32_t sc[CB];
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
-                    x[t] = half + min(t * 16 + r, a.T - 1) * kRow + p * (G / 2) + at * (G * 2);
+                    x[t] = half + min(t * 16 + r, a.T - 1) * kRow + quarter<G>(lane) * (G / 2) + at * (G * 2);
 #pragma unroll
                 for (int c = 0; c < CB; ++c)
                     sc[c] = spread(scales[j / 4][c], j, lane);
                 add_group<Tx, G>(acc, w[j], sc, x,
                                  reinterpret_cast<const float *>(half + a.T * kRow) + at * (TB * 16) + p * 4, base);
             }
+            if (j % kPair<G> == kPair<G> - 1) {
 #pragma unroll
-            for (int c = 0; c < CB; ++c)
-                w[j][c] = load_codes(a, q, c, j, lane);
+                for (int c = 0; c < CB; ++c)
+                    load_codes(a, q, w, c, j - j % kPair<G>, lane);
+            }
         }
 #pragma unroll
         for (int j = 0; j < H / 4; ++j)
@@ -476,7 +549,7 @@ __global__ void __launch_bounds__(512, TB == 1 ? 4 : 2) w4_chunk_kernel(W4FewArg
             for (int c = 0; c < CB; ++c)
                 scales[j][c] = next[j][c];
         if (last)
-            finish<WAVES>(a, pl, turn, acc, s_red);
+            finish<WAVES>(a, SPLIT, turn, acc, reinterpret_cast<f32x4 (*)[TB][CB][64]>(lds));
         turn = next_turn;
         b = next_b;
     }
@@ -497,14 +570,15 @@ hipError_t start(Kern kern, LdsAllowed &allowed, const W4FewArgs &a, const Plan 
 
 // The plan for `waves` waves a workgroup and `resident` workgroups on the chip
 // whose split takes the least time: rounds times groups a wave.
-Plan choose(const W4FewArgs &a, int groups, int held, int waves, int cb, int resident, int max_split)
+Plan choose(const W4FewArgs &a, int units, int waves, int cb, int resident, int max_split, int step = 1)
 {
+    constexpr int held = 4;     // units of 128 columns in a batch
     Plan pl{};
     long long best = LLONG_MAX;
-    for (int split = 0; split <= max_split; ++split) {
+    for (int split = 0; split <= max_split; split += step) {
         const int per = (waves >> split) * 16 * cb;
         const long long turns = ((long long)a.N + per - 1) / per, rounds = (turns + resident - 1) / resident;
-        const long long each = (groups + (1 << split) - 1) >> split;
+        const long long each = (units + (1 << split) - 1) >> split;
         const long long cost = rounds * (each * 4 + (split ? 6 : 2));
         if (cost < best) {
             best = cost;
@@ -521,22 +595,29 @@ hipError_t whole(const W4FewArgs &a, size_t lds, hipStream_t st)
 {
     static LdsAllowed allowed;
     const int resident = WAVES == 8 ? 512 : 256;
-    Plan pl = choose(a, a.K / G, kHeld<G>, WAVES, CB, resident, WAVES == 8 ? 3 : 4);
+    Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, WAVES == 8 ? 3 : 4);
     pl.magic = (uint32_t)(((1ull << 32) + a.K / 8 - 1) / (a.K / 8));
     return start(w4_whole_kernel<Tx, G, TL, WAVES, TB, CB>, allowed, a, pl, lds, resident, WAVES * 64, st);
 }
 
-template <class Tx, int G, bool TL, int TB, int CB>
+template <class Tx, int G, bool TL, int WAVES, int TB, int CB, int M>
 hipError_t chunked(const W4FewArgs &a, hipStream_t st)
 {
+    // M = 1: one, two or four waves share a chunk; M = 4: one, four or sixteen
+    constexpr int kStep = M == 1 ? 1 : 2, resident = 256, threads = WAVES * 64;
     static LdsAllowed allowed[3];
-    const size_t lds = 2 * ((size_t)a.T * (64 * 16 + 16) + kHeld<G> * TB * 64);
-    const int resident = TB == 1 && lds + 8 * CB * 1024 <= kLds / 2 ? 512 : 256;
-    const Plan pl = choose(a, a.K / G, kHeld<G>, 8, CB, resident, 2);
-    switch (pl.split) {
-    case 0: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 0>, allowed[0], a, pl, lds, resident, 512, st);
-    case 1: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 1>, allowed[1], a, pl, lds, resident, 512, st);
-    default: return start(w4_chunk_kernel<Tx, G, TL, TB, CB, 2>, allowed[2], a, pl, lds, resident, 512, st);
+    const size_t need = 2 * ((size_t)a.T * (64 * M * 16 + 16) + kHeld<G> * M * TB * 64);
+    const size_t lds = need > WAVES * TB * CB * 1024 ? need : WAVES * TB * CB * 1024;
+    const Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, 2 * kStep, kStep);
+    switch (pl.split / kStep) {
+    case 0:
+        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, 0>, allowed[0], a, pl, lds, resident, threads, st);
+    case 1:
+        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, kStep>, allowed[1], a, pl, lds, resident, threads,
+                     st);
+    default:
+        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, 2 * kStep>, allowed[2], a, pl, lds, resident,
+                     threads, st);
     }
 }
 
@@ -549,9 +630,9 @@ hipError_t by_tokens(const W4FewArgs &a, hipStream_t st)
             return whole<Tx, G, TL, 8, 1, 1>(a, lds, st);
         if (lds + 16 * 1024 <= kLds)
             return whole<Tx, G, TL, 16, 1, 1>(a, lds, st);
-        return chunked<Tx, G, TL, 1, 2>(a, st);
+        return chunked<Tx, G, TL, 16, 1, 1, 4>(a, st);
     }
-    return a.T <= 32 ? chunked<Tx, G, TL, 2, 2>(a, st) : chunked<Tx, G, TL, 4, 2>(a, st);
+    return a.T <= 32 ? chunked<Tx, G, TL, 16, 2, 1, 1>(a, st) : chunked<Tx, G, TL, 8, 4, 2, 1>(a, st);
 }
 
 template <class Tx>
