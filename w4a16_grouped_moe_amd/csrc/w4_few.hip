@@ -46,6 +46,13 @@ __device__ inline typename Codes<Tx>::vec codes8(uint32_t w, uint32_t base)
     return __builtin_bit_cast(typename Codes<Tx>::vec, u32x4{to(0), to(4), to(8), to(12)});
 }
 
+// Eight values in the codes' order.
+__device__ inline uint4 in_code_order(uint4 v)
+{
+    return make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                      __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
+}
+
 __device__ inline f32x4 mfma(f16x8 a, f16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -97,7 +104,7 @@ template <class Tx>
 __device__ inline uint4 get_x(const W4FewArgs &a, int t, int k8)
 {
     uint4 v;
-    __builtin_memcpy(&v, (const Tx *)a.x + (size_t)t * a.ldx + k8 * 8, 16);
+    __builtin_memcpy(&v, (const char *)a.x + (size_t)t * a.ldx * sizeof(Tx) + (uint32_t)k8 * 16u, 16);
     return v;
 }
 
@@ -222,7 +229,8 @@ __device__ inline uint32_t spread(uint32_t v, int j, int lane)
 }
 
 // One group: its sums of 16 TB tokens by 16 CB channels, scaled, onto acc. x: the
-// lane's first vector of each token block in LDS; sums: the group's sums of x.
+// lane's first vector of each token block in LDS; sums: the group's sums of x. The
+// MFMA sums begin at -(16 + z) sum x.
 template <class Tx, int G, int TB, int CB>
 __device__ inline void add_group(f32x4 (&acc)[TB][CB], const Frag<G> (&w)[CB], const uint32_t (&scales)[CB],
                                  const char *const (&x)[TB], const float *sums, uint32_t base)
@@ -230,10 +238,12 @@ __device__ inline void add_group(f32x4 (&acc)[TB][CB], const Frag<G> (&w)[CB], c
     typedef typename Codes<Tx>::vec vec;
     f32x4 sum[TB][CB];
 #pragma unroll
-    for (int t = 0; t < TB; ++t)
+    for (int t = 0; t < TB; ++t) {
+        const f32x4 xs = *reinterpret_cast<const f32x4 *>(sums + t * 16);
 #pragma unroll
         for (int c = 0; c < CB; ++c)
-            sum[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            sum[t][c] = (-16.0f - half_bits((uint16_t)(scales[c] >> 16))) * xs;
+    }
 #pragma unroll
     for (int i = 0; i < G / 32; ++i) {
         vec q[CB];
@@ -249,13 +259,10 @@ __device__ inline void add_group(f32x4 (&acc)[TB][CB], const Frag<G> (&w)[CB], c
         }
     }
 #pragma unroll
-    for (int c = 0; c < CB; ++c) {
-        const float s = half_bits((uint16_t)scales[c]);
-        const float sz = s * (16.0f + half_bits((uint16_t)(scales[c] >> 16)));
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
-            acc[t][c] += s * sum[t][c] - sz * *reinterpret_cast<const f32x4 *>(sums + t * 16);
-    }
+        for (int c = 0; c < CB; ++c)
+            acc[t][c] += half_bits((uint16_t)scales[c]) * sum[t][c];
 }
 
 // A turn's results from its waves' sums. With waves that share channels these
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
         for (int j = 0; j < kAhead; ++j) {
             if (i0 + j * WAVES * 64 < total) {
                 const float s = group_sum<Tx, G>(v[j]);
-                *reinterpret_cast<uint4 *>(lds + t[j] * row + k8[j] * 16) = permute8(v[j]);
+                *reinterpret_cast<uint4 *>(lds + t[j] * row + k8[j] * 16) = in_code_order(v[j]);
                 if (k8[j] % (G / 8) == 0)
                     sums[k8[j] / (G / 8) * (TB * 16) + t[j]] = s;
             }
@@ -449,36 +456,41 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kern
         const bool live = turn < pl.turns;
         return Weights<G, TL, CB>(a, live ? (turn * sets + set) * 16 * CB : 0, live, b * H, parts, part);
     };
-    // this thread's vectors of a chunk: 64 neighbouring ones of a row per wave
-    uint4 held[kMine];
-    const int chunks = (groups + H * M - 1) / (H * M);
+    // This thread's vectors of a chunk: 64 neighbouring ones of a row per wave. Where
+    // a batch takes several chunks, those of two lie ready, in turn: an even number of
+    // chunks, the last one maybe past K, keeps the turns in step with the batches.
+    constexpr int kDepth = kEach * 2 <= H ? 2 : 1;
+    uint4 held[kDepth][kMine];
+    const int chunks = ((groups + H * M - 1) / (H * M) + kDepth - 1) / kDepth * kDepth;
     auto row_of = [&](int i) { return (i * WAVES + wave) / M; };
     const int mine = wave % M * 64 + lane;           // its column of vectors, the same in each row: M divides WAVES
-    auto fetch = [&](int chunk) {
+    auto fetch = [&](int chunk, uint4 (&to)[kMine]) {
         const int k8 = min(chunk * kWide + mine, a.K / 8 - 1);      // past K: not met by a group
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
             if (row_of(i) < a.T)
-                held[i] = get_x<Tx>(a, row_of(i), k8);
+                to[i] = get_x<Tx>(a, row_of(i), k8);
     };
-    auto store = [&](char *at) {
+    auto store = [&](char *at, const uint4 (&from)[kMine]) {
         float *sums = reinterpret_cast<float *>(at + a.T * kRow);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int t = row_of(i);
             if (t < a.T) {
-                const float s = group_sum<Tx, G>(held[i]);
-                *reinterpret_cast<uint4 *>(at + t * kRow + mine * 16) = permute8(held[i]);
+                const float s = group_sum<Tx, G>(from[i]);
+                *reinterpret_cast<uint4 *>(at + t * kRow + mine * 16) = in_code_order(from[i]);
                 if (lane % (G / 8) == 0)
                     sums[mine / (G / 8) * (TB * 16) + t] = s;
             }
         }
     };
 
-    int turn = blockIdx.x, chunk = 0, side = 0;
+    int turn = blockIdx.x, chunk = kDepth - 1, side = 0;
     Frag<G> w[H][CB];
     uint32_t scales[H / 4][CB];
-    fetch(0);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        fetch(d, held[d]);
     {
         const auto q = source(turn, 0);
 #pragma unroll
@@ -515,10 +527,11 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kern
             if (i % kEach == 0 && i / kEach < chunks) {
                 // the chunk's columns, which the loads have brought, into the half
                 // that was read last before the barrier before this one
+                uint4 (&these)[kMine] = held[j / kEach % kDepth];
                 side ^= 1;
-                store(lds + side * bytes);
+                store(lds + side * bytes, these);
                 chunk = chunk + 1 < chunks ? chunk + 1 : 0;
-                fetch(chunk);
+                fetch(chunk, these);
                 __syncthreads();
             }
             const int u = group_of<G>(i, parts, part);
