@@ -620,9 +620,9 @@ typedef struct {
  *   out     device, out_type (DGW4_F32 or `type`) [R, V] (output), rows ld_out
  *           elements apart, aligned to its element; rounded to its type once;
  *           elements between the rows are left as they are. out == logits
- *           with the same type and row distance is the call in place (what no
- *           rule changes is not written then); else the rows must not overlap
- *           (DGW4_ERR_INVALID_ARG)
+ *           with the same type and row distance is the call in place (without
+ *           a scale it reads and writes only the 16 bytes around what a rule
+ *           changes); else the rows must not overlap (DGW4_ERR_INVALID_ARG)
  *   R >= 0 (0: a no-op), 1 <= V < 2^30 and R * V < 2^40 (more:
  *   DGW4_ERR_UNSUPPORTED)
  * Bit-exact and deterministic. Enqueued on `stream`, no host sync.

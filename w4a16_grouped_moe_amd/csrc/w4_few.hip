@@ -70,6 +70,7 @@ __device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast
 // (1 << split)-th 128 columns of K.
 struct Plan {
     int split, turns, batches;
+    int tokens;                 // of a workgroup: blockIdx.y says which
     uint32_t magic;             // of the division by the vectors of a row (whole K in LDS)
 };
 
@@ -118,6 +119,16 @@ __device__ inline float pair_sum(uint32_t w, float s)
         return __builtin_amdgcn_fdot2(v, one, s, false);
     else
         return __builtin_amdgcn_fdot2_f32_bf16(v, one, s, false);
+}
+
+// The call of this workgroup's tokens alone.
+__device__ inline W4FewArgs own_tokens(W4FewArgs a, int tokens)
+{
+    const int t0 = (int)blockIdx.y * tokens;
+    a.x = (const char *)a.x + (size_t)t0 * a.ldx * 2;
+    a.y = (char *)a.y + (size_t)t0 * a.ldy * (a.y_type == DGW4_F32 ? 4 : 2);
+    a.T = min(tokens, a.T - t0);
+    return a;
 }
 
 template <int CTRL>
@@ -326,11 +337,13 @@ __device__ inline void finish(const W4FewArgs &a, int split, int turn, const f32
 // All activations in LDS, once: rows 16 bytes off the bank period, so that the 16
 // rows of a fragment fall on all banks.
 template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
-__global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Plan pl)
+__global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs all, Plan pl)
 {
+    const W4FewArgs a = own_tokens(all, pl.tokens);
     constexpr int H = kHeld<G>;
     extern __shared__ __attribute__((aligned(16))) char lds[];     // [T][row], then [K/G][16 TB] sums
     __shared__ f32x4 s_red[WAVES][1][CB][64];
+    static_assert(sizeof s_red <= kLdsStatic, "the LDS allowance counts on it");
     const int lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int parts = 1 << pl.split, part = wave & (parts - 1), set = wave >> pl.split, sets = WAVES >> pl.split;
@@ -440,8 +453,9 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs a, Pl
 // The activations M x 512 columns at a time, in two halves of LDS: while one is
 // worked on, the next columns are on their way into registers.
 template <class Tx, int G, bool TL, int WAVES, int TB, int CB, int M, int SPLIT>
-__global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kernel(W4FewArgs a, Plan pl)
+__global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kernel(W4FewArgs all, Plan pl)
 {
+    const W4FewArgs a = own_tokens(all, pl.tokens);
     constexpr int H = kHeld<G>, kWide = 64 * M, kRow = kWide * 16 + 16, kMine = TB * 16 * M / WAVES;
     constexpr int parts = 1 << SPLIT, sets = WAVES >> SPLIT, kEach = H * M >> SPLIT;   // a wave's groups of a chunk
     static_assert(kEach >= kPair<G>, "a wave has 128 columns of each chunk");
@@ -577,7 +591,8 @@ hipError_t start(Kern kern, LdsAllowed &allowed, const W4FewArgs &a, const Plan 
     const hipError_t err = allow_lds_here(kern, lds, allowed);
     if (err != hipSuccess)
         return err;
-    kern<<<dim3(pl.turns < resident ? pl.turns : resident), dim3(threads), lds, st>>>(a, pl);
+    const dim3 grid(pl.turns < resident ? pl.turns : resident, (a.T + pl.tokens - 1) / pl.tokens);
+    kern<<<grid, dim3(threads), lds, st>>>(a, pl);
     return hipGetLastError();
 }
 
@@ -604,24 +619,26 @@ Plan choose(const W4FewArgs &a, int units, int waves, int cb, int resident, int 
 }
 
 template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
-hipError_t whole(const W4FewArgs &a, size_t lds, hipStream_t st)
+hipError_t whole(const W4FewArgs &a, int tokens, size_t lds, hipStream_t st)
 {
     static LdsAllowed allowed;
     const int resident = WAVES == 8 ? 512 : 256;
     Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, WAVES == 8 ? 3 : 4);
+    pl.tokens = tokens;
     pl.magic = (uint32_t)(((1ull << 32) + a.K / 8 - 1) / (a.K / 8));
     return start(w4_whole_kernel<Tx, G, TL, WAVES, TB, CB>, allowed, a, pl, lds, resident, WAVES * 64, st);
 }
 
 template <class Tx, int G, bool TL, int WAVES, int TB, int CB, int M>
-hipError_t chunked(const W4FewArgs &a, hipStream_t st)
+hipError_t chunked(const W4FewArgs &a, int tokens, hipStream_t st)
 {
     // M = 1: one, two or four waves share a chunk; M = 4: one, four or sixteen
     constexpr int kStep = M == 1 ? 1 : 2, resident = 256, threads = WAVES * 64;
     static LdsAllowed allowed[3];
-    const size_t need = 2 * ((size_t)a.T * (64 * M * 16 + 16) + kHeld<G> * M * TB * 64);
+    const size_t need = 2 * ((size_t)tokens * (64 * M * 16 + 16) + kHeld<G> * M * TB * 64);
     const size_t lds = need > WAVES * TB * CB * 1024 ? need : WAVES * TB * CB * 1024;
-    const Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, 2 * kStep, kStep);
+    Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, 2 * kStep, kStep);
+    pl.tokens = tokens;
     switch (pl.split / kStep) {
     case 0:
         return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, 0>, allowed[0], a, pl, lds, resident, threads, st);
@@ -634,18 +651,33 @@ hipError_t chunked(const W4FewArgs &a, hipStream_t st)
     }
 }
 
+// tokens: of a workgroup, at most 16.
+template <class Tx, int G, bool TL>
+hipError_t one_block(const W4FewArgs &a, int tokens, hipStream_t st)
+{
+    const size_t lds = (size_t)tokens * (a.K * 2 + 16) + (size_t)(a.K / G) * 64;
+    if (lds + 8 * 1024 <= kLds / 2)
+        return whole<Tx, G, TL, 8, 1, 1>(a, tokens, lds, st);
+    if (lds + 16 * 1024 <= kLds)
+        return whole<Tx, G, TL, 16, 1, 1>(a, tokens, lds, st);
+    return chunked<Tx, G, TL, 16, 1, 1, 4>(a, tokens, st);
+}
+
+// More than 16 tokens share each weight's unpacking in one workgroup, unless there
+// are so few channels that workgroups of 16 or of 32 tokens each (which read the
+// same weights, from the caches but for one of them) still run all at once: 64
+// tokens, K = 2816: 1024 channels 7 us in blocks of 16, 11 in 32, 18 whole; 8192
+// channels 26, 12 and 19; 16384 channels 36, 24 and 21.
 template <class Tx, int G, bool TL>
 hipError_t by_tokens(const W4FewArgs &a, hipStream_t st)
 {
-    if (a.T <= 16) {
-        const size_t lds = (size_t)a.T * (a.K * 2 + 16) + (size_t)(a.K / G) * 64;
-        if (lds + 8 * 1024 <= kLds / 2)
-            return whole<Tx, G, TL, 8, 1, 1>(a, lds, st);
-        if (lds + 16 * 1024 <= kLds)
-            return whole<Tx, G, TL, 16, 1, 1>(a, lds, st);
-        return chunked<Tx, G, TL, 16, 1, 1, 4>(a, st);
-    }
-    return a.T <= 32 ? chunked<Tx, G, TL, 16, 2, 1, 1>(a, st) : chunked<Tx, G, TL, 8, 4, 2, 1>(a, st);
+    constexpr int kChip = 256;
+    const long long by16 = (a.T + 15) / 16 * ((a.N + 15LL) / 16), by32 = (a.T + 31) / 32 * ((a.N + 63LL) / 64);
+    if (a.T <= 16 || by16 <= kChip)
+        return one_block<Tx, G, TL>(a, a.T < 16 ? a.T : 16, st);
+    if (a.T <= 32 || by32 <= kChip)
+        return chunked<Tx, G, TL, 16, 2, 1, 1>(a, a.T < 32 ? a.T : 32, st);
+    return chunked<Tx, G, TL, 8, 4, 2, 1>(a, a.T, st);
 }
 
 template <class Tx>
