@@ -15,6 +15,13 @@
 // A wave's part of a row (the maximum, its first place, sums of exp relative to
 // it, the best score) goes to the workspace; a second kernel joins a row's parts.
 // Every order is fixed, so results are bitwise reproducible.
+//
+// Bounds: adjusting is a copy, 256 x 262144 fp32 102 us (5.3 TB/s; in place, with
+// nothing changed but a few columns, 64 x 262144 20 us). The sampler without rules
+// reads 6.1 TB/s (256 x 262144, entropy and argmax 44 us); history costs it a third
+// to a half on top, in the steps that make the words (64 rows of own sequences of
+// 1000 tokens: 17 -> 30 us) and in the columns with words (256 rows of 4
+// sequences of 8000 tokens: 85 us, 64 without those columns' arithmetic).
 #include "element_types.hpp"
 #include "logit_rules.hpp"
 #include "sampler_common.hpp"

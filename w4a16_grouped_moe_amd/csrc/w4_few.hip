@@ -9,8 +9,30 @@
 //
 // v_mfma_f32_16x16x32 takes 16 tokens as rows and 16 channels as columns: a lane
 // holds one channel, so one scale and one zero point serve its four outputs. Of
-// a group, lane (p, r) holds channel r's quarter p: its 16 (or 8) bytes are
-// two nibbles a byte in K order, eight nibbles a dword.
+// a group, lane (p, r) holds a quarter of channel r's: its 16 (or 8) bytes are
+// two nibbles a byte in K order, eight nibbles a dword. The group's MFMA sum begins
+// at -(16 + z) sum_k x, with sum_k x formed once when x goes to LDS, and meets the
+// scale in one fma.
+//
+// At few tokens the weights' read is all the work. A wave holds 512 columns of 16
+// channels and refills each register with the next 512's as soon as it is used;
+// scales and zero points come with one load each for four groups, a lane's quarter
+// saying which, and are spread by a permute (a load of two bytes for each group
+// took 84 us where this takes 68: 1 token, 262144 channels, K = 2816, 392 MB;
+// without any scales 61). The weights' buffer resources are forced into scalar
+// registers (74 -> 68 us without per-lane loops around the loads). K is split over
+// 1 to 16 waves of a workgroup by an estimate, rounds of the chip times groups a
+// wave; their sums meet in LDS. Larger batches held (8 groups a wave) were slower
+// at small sizes and level at the LM head.
+//
+// Up to 16 tokens whose x fits LDS whole (w4_whole_kernel): tiled weights, g 128,
+// in a graph: 1 token x 4096 channels x 2816 5.0 us, 16 x 11264 x 4096 11.8 (the
+// activations' way into every workgroup's LDS, 131 KB, is part of it), LM head 1 /
+// 5 / 16 tokens 68 / 72 / 79 us (5.8 / 5.4 / 5.0 TB/s). Else x goes through LDS in
+// chunks (w4_chunk_kernel): 2 x 4096 x 65536 33 us, LM head 32 / 64 tokens 103 /
+// 151 us, where unpacking, the scales' fma and the MFMA share the time (a chunk of
+// 512 columns of 64 tokens takes a workgroup 2.2 us, 0.8 for each group's products
+// of a wave, the rest the staging of x).
 #include "gemm_common.hpp"
 #include "step_end.hpp"
 
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(WAVES * 64, 4) w4_whole_kernel(W4FewArgs all, 
                 load_codes(a, q, w, c, j, lane);
         }
     }
-    constexpr int kAhead = WAVES == 16 ? 8 : 4;      // vectors of x a thread has on their way at once
+    constexpr int kAhead = 4;        // vectors of x a thread has on their way at once
     const int wide = a.K / 8, total = a.T * wide;
     for (int i0 = threadIdx.x; i0 < total; i0 += kAhead * WAVES * 64) {
         uint4 v[kAhead];
