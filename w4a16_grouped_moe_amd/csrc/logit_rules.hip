@@ -201,6 +201,21 @@ __device__ inline uint32_t allowed(const uint32_t *mask, int c, int V)
     return mask && c < V ? mask[c >> 5] >> (c & 31) : ~0u;
 }
 
+// l where bit i of bits is set, else -inf.
+__device__ inline float kept(float l, uint32_t bits, int i)
+{
+    const uint32_t all = (uint32_t)((int32_t)(bits << (31 - i)) >> 31);
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, l) & all) | (0xFF800000u & ~all));
+}
+
+// The largest of three. (fmaxf would have the compiler quiet each logit first.)
+__device__ inline float max3(float a, float b, float c)
+{
+    float v;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(v) : "v"(a), "v"(b), "v"(c));
+    return v;
+}
+
 // Which of a thread's columns have a word: bit k * W + i for column i of vector k,
 // whose words lie from words + k * step on.
 template <int W, int N>
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
             vec y;
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                y[i] = from_f32<Ty>(bits[k] >> i & 1 ? l[k * W + i] : -INFINITY);
+                y[i] = from_f32<Ty>(kept(l[k * W + i], bits[k], i));
             if (c + W <= a.V) {
                 if constexpr (SPARSE)
                     *reinterpret_cast<vec *>(out + c) = y;
@@ -357,12 +372,15 @@ __global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
         if (r + 1 < end)
             read_all<Tx, N>(x, row + a.ld, mine, 64 * W, a.V, inside);
         follow_rules<W, N>(l, needs, own, 64 * W, q);
+        if (mask || !inside) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                l[e] = kept(l[e], bits[e / W], e % W);
+        }
         float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            l[e] = bits[e / W] >> (e % W) & 1 ? l[e] : -INFINITY;
-            top = fmaxf(top, l[e]);
-        }
+        for (int e = 0; e < E; e += 2)
+            top = max3(top, l[e], l[e + 1]);
         Partial p;
         p.m = across_max(top);
         const float m = p.m > -INFINITY ? p.m : 0.0f;
