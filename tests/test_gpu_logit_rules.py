@@ -193,6 +193,81 @@ def test_many_rows():
     assert np.array_equal(am.cpu().numpy(), want.argmax(1))
 
 
+def test_offsets_past_32_bits():
+    # more logits than 32 bits count, tokens at the end of long rows
+    R, V = 9, 1 << 28
+    x = torch.zeros((R, V), dtype=F16, device="cuda")
+    at = torch.tensor([0, 1, V // 2 + 3, V - 2, V - 1], device="cuda")
+    x[:, at] = torch.tensor([1.0, 2.0, 4.0, 3.0, 8.0], dtype=F16, device="cuda")
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    rules = dg.LogitRules(tokens=i([[V - 1, V - 1, V - 2]]).expand(R, 3).contiguous(), lengths=i([3] * R),
+                          presence=torch.full((R,), 1.0, device="cuda"),
+                          frequency=torch.full((R,), 2.0, device="cuda"))
+    out = dg.adjust_logits(x, rules, dtype=F16)
+    assert (out[:, at].float() == torch.tensor([1.0, 2.0, 4.0, 0.0, 3.0], device="cuda")).all()
+    assert int(torch.count_nonzero(out[R - 1])) == 4
+    h, _, am = dg.sample_adjusted(x, rules, draw=False)
+    assert (am == V // 2 + 3).all()
+    # Nearly all of the weight is on the zeros. A row has 2^18 parts, 1024 one after
+    # the other in a thread of the join: z and s are off by at most 1324 u32 of
+    # themselves, and |s / z| is below 9.
+    z = V - 4 + sum(np.exp([1.0, 2.0, 4.0, 3.0]))
+    want = np.log(z) - sum(v * np.exp(v) for v in (1.0, 2.0, 4.0, 3.0)) / z
+    assert np.abs(h.cpu().numpy() - want).max() <= 1.01 * (1 + 2 * 9) * 1324 * 2.0 ** -24
+
+
+def test_two_host_threads():
+    # two threads on streams of their own, the same rules object
+    import threading
+    rng = np.random.default_rng(16)
+    l, u, rules = _case(rng, 8, 30000, F32, L=200, bias=3, mask=True)
+    x = l.cuda()
+    want = dg.sample_adjusted(x, rules, 5)
+    adj = dg.adjust_logits(x, rules)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got, a = dg.sample_adjusted(x, rules, 5), dg.adjust_logits(x, rules)
+                torch.cuda.current_stream().synchronize()
+                if not (same_bits(got[0], want[0]) and torch.equal(got[1], want[1]) and same_bits(a, adj)):
+                    bad.append("differs")
+        except Exception as e:
+            bad.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_two_graphs_share_a_workspace():
+    # replayed one after the other on one stream
+    rng = np.random.default_rng(17)
+    cases = [_case(rng, R, V, F32, L=60, mask=True) for R, V in ((6, 50000), (2, 200000))]
+    n = max(dg.sample_adjusted_workspace_bytes(*c[0].shape) for c in cases)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    xs = [c[0].cuda() for c in cases]
+    for x, c in zip(xs, cases):
+        dg.sample_adjusted(x, c[2], 7, workspace=ws)
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x, c in zip(xs, cases):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(dg.sample_adjusted(x, c[2], 7, workspace=ws))
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        for k, (l, u, _) in enumerate(cases):
+            rules_ref.check_sample(rules_ref.adjusted(l, u), 7, *got[k])
+
+
 def test_counts():
     # one token very often, in the prompt and after it
     L, V = 100000, 5000

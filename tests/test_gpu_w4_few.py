@@ -202,3 +202,23 @@ def test_refusals():
     with pytest.raises(dg.Dgw4Error, match="UNSUPPORTED"):
         dg.w4a16_linear_few(torch.zeros((65, 128), dtype=F16, device="cuda"), w)
     assert dg.w4a16_linear_few(x[:0], w).shape == (0, 32)
+
+
+def test_offsets_past_32_bits():
+    # weights and scales past 2 GiB, rows of x and y far apart: the last channels
+    # of the last tokens
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N, K, T = 1100003, 4096, 3
+    q = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=torch.uint8, generator=g)
+    s = (torch.rand((N, K // 64), device="cuda", generator=g) * 0.01).half()
+    z = torch.randint(0, 16, (N, K // 64), device="cuda", generator=g).half()
+    assert q.numel() > 2 ** 31
+    wide = torch.zeros((T, 800_000_000), device="cuda", dtype=torch.float16)
+    x = wide[:, -K:]
+    x.copy_(torch.randn((T, K), device="cuda", generator=g))
+    out = torch.zeros((T, 800_000_000), device="cuda", dtype=torch.float16)
+    y = out[:, -N:]
+    dg.w4a16_linear_few(x, (q, s, z, 64), out=y)
+    for part in (slice(0, 40), slice(524270, 524310), slice(N - 40, N)):
+        _check(y[:, part], x.cpu(), [v[part].cpu().numpy() for v in (q, s, z)], 64)
+    assert (out[:, :-N] == 0).all()

@@ -238,11 +238,18 @@ __device__ inline void follow_rules(float (&l)[N * W], uint32_t need, const uint
 {
     while (__ballot(need != 0)) {
         const int at = need ? __builtin_ctz(need) : N * W;
-        float v = l[0];
+        const uint32_t word = words[need ? at / W * step + at % W : 0];
+        // column `at` by its bits, the lowest first
+        float pick[N * W];
 #pragma unroll
-        for (int e = 1; e < N * W; ++e)
-            v = at == e ? l[e] : v;
-        v = adjusted(v, words[need ? at / W * step + at % W : 0], q);
+        for (int e = 0; e < N * W; ++e)
+            pick[e] = l[e];
+#pragma unroll
+        for (int half = N * W / 2, bit = 1; half > 0; half /= 2, bit *= 2)
+#pragma unroll
+            for (int e = 0; e < half; ++e)
+                pick[e] = at & bit ? pick[2 * e + 1] : pick[2 * e];
+        const float v = adjusted(pick[0], word, q);
 #pragma unroll
         for (int e = 0; e < N * W; ++e)
             l[e] = at == e ? v : l[e];
