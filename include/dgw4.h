@@ -537,9 +537,10 @@ DGW4_API int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, lo
  * Sums are fp32: codes enter as the exact values 16 + q, the group's
  * (16 + z) sum_k x is taken off its sum, the scale is applied to the
  * difference; y is rounded to its type once. Results do not depend on timing,
- * repeated calls give identical bits, and a token's results depend on its own
- * row of x only. A token with a NaN or an infinity in x has NaN or infinite
- * results; finite ones below 2^100 cannot overflow on the way.
+ * repeated calls give identical bits, and for a given T a token's results
+ * depend on its own row of x only. A token with a NaN or an infinity in x has
+ * NaN or infinite results; finite values below 2^100 do not overflow before the
+ * scale is applied.
  *   x   device, x_type DGW4_F16 or DGW4_BF16 [T, K], rows ldx elements apart
  *       (ldx >= K), aligned to its element
  *   q, s, z, g  one matrix [N, K] as for dgw4_w4a16_linear (16-byte aligned;

@@ -789,12 +789,17 @@ def w4a16_linear_few(x: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
         raise ValueError(f"group size {g} with its flags is not valid")
     pq, ps, pz = _flat(q, "q", _U8, d), _flat(s, "s", _F16, d), _flat(z, "z", _F16, d)
     N = q.shape[0]
-    if q.shape != (N, K // 2) or s.shape != (N, K // _group(g)) or z.shape != s.shape:
+    scales = (N, K // _group(g))
+    if q.shape != (N, K // 2) or s.shape != scales or z.shape != scales:
         raise ValueError(f"packed shapes {tuple(q.shape)}, {tuple(s.shape)}, {tuple(z.shape)} do not match "
                          f"x {tuple(x.shape)}")
     if N >> 31:
         _sizes(N=N)
-    out, py, ldy = _w8a8_out(x, T, N, dtype or x.dtype, out, d)
+    if out is None and (dtype is None or dtype is x.dtype):
+        out = x.new_empty((T, N))                # the shortest way to an output
+        py, ldy = out.data_ptr(), N
+    else:
+        out, py, ldy = _w8a8_out(x, T, N, dtype, out, d)
     _call("dgw4_w4a16_linear_few", d, px, _TYPES[x.dtype], T, K, ldx, pq, ps, pz, N, g, py,
           _TYPES[out.dtype], ldy)
     return out
