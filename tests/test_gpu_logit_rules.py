@@ -370,3 +370,15 @@ def test_refusals():
         dg.sample_adjusted(x, none, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert dg.adjust_logits(x[:0], none).shape == (0, 100)
     assert dg.sample_adjusted(x[:0], none)[2].shape == (0,)
+
+
+def test_as_many_rows_as_an_int_counts():
+    """2^31 - 1 rows of one column: the last rows are changed as the others."""
+    R = 2**31 - 1
+    x = torch.empty(R, 1, device="cuda", dtype=torch.float16)
+    at = x.view(-1)
+    at.fill_(1.0)
+    ends = torch.arange(-2000, 2000, device="cuda")
+    at[ends] = (ends % 2000).to(torch.float16)
+    y = dg.adjust_logits(x, dg.LogitRules(), dtype=torch.float16)
+    assert torch.equal(y, x)

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
     const int c0 = tile * kTile;
     const uint32_t *own = words + (HIST ? (int)threadIdx.x * W : 0);        // of this thread's first vector
     constexpr uint32_t kAll = (1u << W) - 1;
-    const int mine = c0 + (int)threadIdx.x * W, end = min(r0 + rows, a.R);
+    const int mine = c0 + (int)threadIdx.x * W, end = r0 + min(rows, a.R - r0);
     const bool inside = c0 + kTile <= a.V;
     const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
     Ty *out = (Ty *)a.out + (long long)r0 * a.ld_out;
@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
 __device__ inline float bounded(float d) { return fmaxf(d, -200.0f); }
 
 template <class Tx, int kThreads, int E, bool HIST>
-__global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4) sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
+__global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
+    sample_adjusted_kernel(LogitArgs a, int tiles, int rows)
 {
     constexpr int W = Wide<Tx>::W, N = E / W, kTile = tile_of(kThreads, E), kWaves = kThreads / 64;
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile : 4];
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile, first = wave * part_of(E);       // the tile's and, in it, the wave's columns
     const uint32_t *own = words + (HIST ? first + lane * W : 0);   // of this lane's first vector
-    const int mine = c0 + first + lane * W, end = min(r0 + rows, a.R);
+    const int mine = c0 + first + lane * W, end = r0 + min(rows, a.R - r0);
     const bool inside = c0 + kTile <= a.V;
     const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
     typename Wide<Tx>::vec x[N];
