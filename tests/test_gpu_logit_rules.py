@@ -82,6 +82,34 @@ def test_sample(R, V, kw):
         assert same_bits(h, h2) and torch.equal(smp, smp2) and torch.equal(am, am2) and torch.equal(am, am3)
 
 
+@pytest.mark.parametrize("V", [9000, 20011])
+def test_columns_with_words_from_few_to_all(V):
+    # runs of n tokens' columns, scattered and side by side, so that waves have
+    # none, few, as many as their lanes take in turns, more than that, and all;
+    # then rows that share those sequences, in any order
+    runs = [0, 1, 63, 64, 65, 127, 128, 129, 130, 500, 1024, V]
+    L = max(runs)
+    rng = np.random.default_rng(V)
+    S = 2 * len(runs)
+    u = rules_ref.random_rules(rng, S, V, L=L, bias=7)
+    for i, n in enumerate(runs):
+        u["tokens"][2 * i, :n] = torch.from_numpy(rng.permutation(min(1024, V))[:n] if n <= 1024
+                                                  else rng.permutation(V)).int()
+        u["tokens"][2 * i + 1, :n] = torch.arange(n).int()
+        u["lengths"][2 * i:2 * i + 2] = n
+    u["prompt_lengths"] = u["lengths"] // 2
+    for R in (S, 400):
+        u["row_seq"] = torch.from_numpy(np.sort(rng.integers(0, S, R)) if R != S else rng.permutation(S)).int()
+        for dtype in TYPES:
+            l = _logits(rng, R, V, dtype, inf=0.01)
+            rules, want, x = _rules(u), rules_ref.adjusted(l, u), l.cuda()
+            assert same_bits(dg.adjust_logits(x, rules), torch.from_numpy(want))
+            rules_ref.check_sample(want, R, *dg.sample_adjusted(x, rules, R))
+            plain = {k: v for k, v in u.items() if k != "scale"}
+            dg.adjust_logits(x, _rules(plain), out=x)
+            assert same_bits(x, torch.from_numpy(rules_ref.adjusted(l, plain)).to(dtype))
+
+
 def test_no_rules():
     # nothing but a copy, and dgw4_sample's own draws
     rng = np.random.default_rng(0)

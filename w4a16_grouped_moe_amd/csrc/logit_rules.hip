@@ -9,19 +9,22 @@
 // that share a sequence share the words. Each logit is read once.
 //
 // The rules' arithmetic costs a lane about thirty instructions, and few columns
-// have a word: a lane takes one such column of its own at a time, until no lane of
-// the wave has one left.
+// have a word: the wave's lanes take those columns in turns of 64, whoever holds
+// them, and the logits go through LDS there and back. (Each lane with its own
+// columns, one at a time, waits for the lane that has most: a canvas of 256 rows
+// and 4 sequences 84 us against 75, 64 histories of 60000 tokens 70 against 65; in
+// place with nothing else changed it was the better by 20 us to 21.)
 //
 // A wave's part of a row (the maximum, its first place, sums of exp relative to
 // it, the best score) goes to the workspace; a second kernel joins a row's parts.
 // Every order is fixed, so results are bitwise reproducible.
 //
-// Bounds: adjusting is a copy, 256 x 262144 fp32 102 us (5.3 TB/s; in place, with
-// nothing changed but a few columns, 64 x 262144 20 us). The sampler without rules
-// reads 6.1 TB/s (256 x 262144, entropy and argmax 44 us); history costs it a third
-// to a half on top, in the steps that make the words (64 rows of own sequences of
-// 1000 tokens: 17 -> 30 us) and in the columns with words (256 rows of 4
-// sequences of 8000 tokens: 85 us, 64 without those columns' arithmetic).
+// Bounds: adjusting is a copy, 256 x 262144 fp32 101 us (5.3 TB/s; in place, with
+// nothing changed but a few columns, 64 x 262144 21 us). The sampler without rules
+// reads 6.4 TB/s (256 x 262144, entropy and argmax 42 us); history costs half or more
+// on top, in the steps that make the words (64 rows of own sequences of 1000
+// tokens: 16 -> 29 us) and in the columns with words and the registers they take
+// (256 rows of 4 sequences of 8000 tokens: 42 -> 64 us, 75 with masks).
 #include "element_types.hpp"
 #include "logit_rules.hpp"
 #include "sampler_common.hpp"
@@ -230,30 +233,94 @@ __device__ inline uint32_t with_words(const uint32_t *words, int step)
     return need;
 }
 
-// A thread's N vectors of W logits after their sequence's rules. need: the columns
-// with a word, as with_words() has them.
+// A wave's columns with words, dealt out over its lanes: lane i has the i-th of each
+// 64, its place in the tile's words and its word. Two turns: one sends the waves of
+// long histories the other way (64 of 60000 tokens: 72 us against 65), three or four
+// take registers from all (canvas of 256 rows in fp16: 100 and 103 us against 96).
+constexpr int kDealt = 2;
+
+struct Dealt {
+    int count;                                   // more than kDealt * 64: not dealt out
+    uint32_t at[kDealt], word[kDealt];
+};
+
+// What the wave's lanes have written to LDS, before any of them reads it.
+__device__ inline void within_wave()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// need: this thread's columns with a word, as with_words() has them, the first at
+// words[own]; list: kDealt * 64 places of the wave's own.
 template <int W, int N>
-__device__ inline void follow_rules(float (&l)[N * W], uint32_t need, const uint32_t *words, int step,
+__device__ inline void deal(Dealt &d, uint32_t need, const uint32_t *words, int own, int step, uint16_t *list)
+{
+    const int lane = threadIdx.x & 63, n = __builtin_popcount(need);
+    int place = 0;
+    d.count = 0;
+#pragma unroll
+    for (int b = 0; 1 << b <= N * W; ++b) {
+        const uint64_t some = __ballot(n >> b & 1);
+        place += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0))
+                 << b;
+        d.count += __builtin_popcountll(some) << b;
+    }
+    if (d.count > kDealt * 64)
+        return;
+    for (; need; need &= need - 1) {
+        const int at = __builtin_ctz(need);
+        list[place++] = (uint16_t)(own + at / W * step + at % W);
+    }
+    within_wave();
+#pragma unroll
+    for (int j = 0; j < kDealt; ++j)
+        if (j * 64 + lane < d.count) {
+            d.at[j] = list[j * 64 + lane];
+            d.word[j] = words[d.at[j]];
+        }
+    within_wave();
+}
+
+// A thread's N vectors of W logits after their sequence's rules. The wave's logits
+// change places with its words, which d holds, and each lane takes the columns
+// dealt to it; where too many have a word, every lane takes all of its own.
+template <int W, int N>
+__device__ inline void follow_rules(float (&l)[N * W], const Dealt &d, uint32_t *words, int own, int step,
                                     const Sequence &q)
 {
-    while (__ballot(need != 0)) {
-        const int at = need ? __builtin_ctz(need) : N * W;
-        const uint32_t word = words[need ? at / W * step + at % W : 0];
-        // column `at` by its bits, the lowest first
-        float pick[N * W];
+    const int lane = threadIdx.x & 63;
+    if (d.count > kDealt * 64) {
 #pragma unroll
-        for (int e = 0; e < N * W; ++e)
-            pick[e] = l[e];
+        for (int e = 0; e < N * W; ++e) {
+            const uint32_t word = words[own + e / W * step + e % W];
+            if (word)
+                l[e] = adjusted(l[e], word, q);
+        }
+    } else if (d.count > 0) {
 #pragma unroll
-        for (int half = N * W / 2, bit = 1; half > 0; half /= 2, bit *= 2)
+        for (int e = 0; e < N * W; e += 4)
+            *reinterpret_cast<uint4 *>(words + own + e / W * step + e % W) =
+                make_uint4(__builtin_bit_cast(uint32_t, l[e]), __builtin_bit_cast(uint32_t, l[e + 1]),
+                           __builtin_bit_cast(uint32_t, l[e + 2]), __builtin_bit_cast(uint32_t, l[e + 3]));
+        within_wave();
 #pragma unroll
-            for (int e = 0; e < half; ++e)
-                pick[e] = at & bit ? pick[2 * e + 1] : pick[2 * e];
-        const float v = adjusted(pick[0], word, q);
+        for (int j = 0; j < kDealt; ++j)
+            if (j * 64 + lane < d.count) {
+                const float v = __builtin_bit_cast(float, words[d.at[j]]);
+                words[d.at[j]] = __builtin_bit_cast(uint32_t, adjusted(v, d.word[j], q));
+            }
+        within_wave();
 #pragma unroll
-        for (int e = 0; e < N * W; ++e)
-            l[e] = at == e ? v : l[e];
-        need &= need - 1;
+        for (int e = 0; e < N * W; e += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(words + own + e / W * step + e % W);
+            l[e] = __builtin_bit_cast(float, v.x);
+            l[e + 1] = __builtin_bit_cast(float, v.y);
+            l[e + 2] = __builtin_bit_cast(float, v.z);
+            l[e + 3] = __builtin_bit_cast(float, v.w);
+        }
+        within_wave();
     }
 #pragma unroll
     for (int e = 0; e < N * W; ++e)
@@ -269,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
     __shared__ __attribute__((aligned(16))) uint32_t words[HIST ? kTile : 4];
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile;
-    const uint32_t *own = words + (HIST ? (int)threadIdx.x * W : 0);        // of this thread's first vector
+    __shared__ uint16_t list[HIST ? kThreads / 64 : 1][kDealt * 64];
+    const int own = HIST ? (int)threadIdx.x * W : 0, wave = (int)threadIdx.x >> 6;   // own: the first vector's words
     constexpr uint32_t kAll = (1u << W) - 1;
     const int mine = c0 + (int)threadIdx.x * W, end = r0 + min(rows, a.R - r0);
     const bool inside = c0 + kTile <= a.V;
@@ -280,6 +348,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
         read_all<Tx, N>(x, row, mine, kThreads * W, a.V, inside);
     int seq = -2;
     uint32_t needs = 0;
+    Dealt d;
+    d.count = 0;
     for (int r = r0; r < end; ++r, row += a.ld, out += a.ld_out) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
@@ -289,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
             bits[k] = allowed<W>(mask, mine + k * kThreads * W, a.V);
         if (HIST && s != seq) {
             enter<kThreads, kTile>(a.rules, s, c0, words);
-            needs = with_words<W, N>(own, kThreads * W);
+            needs = with_words<W, N>(words + own, kThreads * W);
+            deal<W, N>(d, needs, words, own, kThreads * W, list[wave]);
         }
         seq = s;
         const Sequence q = sequence(a.rules, s);
@@ -308,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kern
         // the next row's, behind this one's arithmetic
         if (!SPARSE && r + 1 < end)
             read_all<Tx, N>(x, row + a.ld, mine, kThreads * W, a.V, inside);
-        follow_rules<W, N>(l, needs, own, kThreads * W, q);
+        follow_rules<W, N>(l, d, words, own, kThreads * W, q);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int c = c0 + (k * kThreads + (int)threadIdx.x) * W;
@@ -347,14 +418,16 @@ __global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int tile = (int)(blockIdx.x % (uint32_t)tiles), r0 = (int)(blockIdx.x / (uint32_t)tiles) * rows;
     const int c0 = tile * kTile, first = wave * part_of(E);       // the tile's and, in it, the wave's columns
-    const uint32_t *own = words + (HIST ? first + lane * W : 0);   // of this lane's first vector
+    __shared__ uint16_t list[HIST ? kWaves : 1][kDealt * 64];
+    const int own = HIST ? first + lane * W : 0;                  // where this lane's first vector's words are
     const int mine = c0 + first + lane * W, end = r0 + min(rows, a.R - r0);
     const bool inside = c0 + kTile <= a.V;
     const Tx *row = (const Tx *)a.logits + (long long)r0 * a.ld;
     typename Wide<Tx>::vec x[N];
     read_all<Tx, N>(x, row, mine, 64 * W, a.V, inside);
     int seq = -2;
-    uint32_t needs = 0;
+    Dealt d;
+    d.count = 0;
     for (int r = r0; r < end; ++r, row += a.ld) {
         const int s = sequence_of(a.rules, r);
         const uint32_t *mask = mask_of(a.rules, r);
@@ -368,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
         }
         if (HIST && s != seq) {
             enter<kThreads, kTile>(a.rules, s, c0, words);
-            needs = with_words<W, N>(own, 64 * W);
+            deal<W, N>(d, with_words<W, N>(words + own, 64 * W), words, own, 64 * W, list[wave]);
         }
         seq = s;
         const Sequence q = sequence(a.rules, s);
@@ -379,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, !HIST ? 6 : sizeof(Tx) == 2 ? 5 : 4)
         // the next row's, behind this one's arithmetic
         if (r + 1 < end)
             read_all<Tx, N>(x, row + a.ld, mine, 64 * W, a.V, inside);
-        follow_rules<W, N>(l, needs, own, 64 * W, q);
+        follow_rules<W, N>(l, d, words, own, 64 * W, q);
         if (mask || !inside) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
