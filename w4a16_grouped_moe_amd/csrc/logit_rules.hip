@@ -37,9 +37,9 @@ namespace {
 
 // Threads of a workgroup. Long histories take the wider one: each workgroup reads
 // its rows' whole histories, so half as many of them read half as much (64
-// sequences of 60000 tokens: 85 -> 71 us, one of 120000: 38 -> 25). Short ones
+// sequences of 60000 tokens: 80 -> 66 us, one of 120000: 37 -> 24). Short ones
 // take the narrower: more workgroups on a compute unit hide each other's steps (a
-// canvas of 4 sequences of 8000: 85 us against 90).
+// canvas of 4 sequences of 8000: 76 us against 80).
 constexpr int kNarrow = 256, kBroad = 512;
 constexpr int kLongHistory = 16384;
 constexpr int kJoin = 256;           // threads that join a row's parts
