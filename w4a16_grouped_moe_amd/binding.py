@@ -898,7 +898,7 @@ def _logits(logits, rules, d: int) -> tuple:
     for name, n in rules._rows:
         if n < R:
             raise ValueError(f"{name}: the rules reach {n} rows, the logits have {R}")
-    if rules._words * 32 < V and rules._c.mask:
+    if rules._words * 32 < V and rules._c.mask_rows:     # (a mask of no words has no address)
         raise ValueError(f"mask has {rules._words} words a row, {V} columns need {(V + 31) // 32}")
     return p, _TYPES[logits.dtype], R, V, ld
 
