@@ -37,3 +37,18 @@ def test_a_mask_of_no_rows_that_no_row_has():
         B._logits(torch.zeros(3, 40), dg.LogitRules(mask=_ints(0, words), mask_row=_ints(3)), HOST)
     with pytest.raises(ValueError, match="reach 0 rows"):
         B._logits(torch.zeros(3, 40), dg.LogitRules(mask=_ints(0, 2)), HOST)
+
+
+def test_rules_of_no_sequences():
+    # a batch none of whose rows has a sequence: biases as well as tokens and scales
+    # are absent then (biases without an address were handed on, which the call refuses)
+    none = dict(tokens=_ints(0, 5), lengths=_ints(0), repetition=torch.zeros(0), scale=torch.zeros(0),
+                bias_ids=_ints(0, 4), bias=torch.zeros(0, 4))
+    for kw in (none, {k: none[k] for k in ("bias_ids", "bias")}):
+        rules = dg.LogitRules(row_seq=torch.full((3,), -1, dtype=torch.int32), **kw)
+        assert (rules._c.sequences, rules._c.n_bias, rules._c.tokens) == (0, 0, None)
+        B._logits(torch.zeros(3, 40), rules, HOST)
+        # the library's own checks (of no rows: nothing is launched)
+        assert dg.lib().dgw4_adjust_logits(None, 0, 0, 40, 40, rules._ref, None, 0, 40, None) == B.OK
+    one = dg.LogitRules(bias_ids=_ints(1, 4), bias=torch.zeros(1, 4))
+    assert (one._c.sequences, one._c.n_bias) == (1, 4)

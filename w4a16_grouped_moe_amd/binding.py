@@ -869,6 +869,8 @@ class LogitRules:
             if ids[2] != c.ld_bias:
                 raise ValueError("bias_ids and bias must have the same row distance")
             S = n
+            if S == 0:                           # no address either: none
+                c.n_bias = 0
         self._words, self._rows = 0, []          # the columns of mask, and how many rows the rules reach
         if row_seq is not None:
             c.row_seq = _flat(row_seq, "row_seq", _I32, d)
