@@ -35,8 +35,7 @@
 // of a wave, the rest the staging of x).
 #include "gemm_common.hpp"
 #include "step_end.hpp"
-
-#include <limits.h>
+#include "w4_few_plan.hpp"
 
 namespace dgw4 {
 namespace {
@@ -86,20 +85,6 @@ __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 }
 
 __device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
-
-// How a call is cut up. A turn is what a workgroup takes at a time: its waves in
-// sets of 1 << split, each set 16 CB channels, the waves of a set every
-// (1 << split)-th 128 columns of K.
-struct Plan {
-    int split, turns, batches;
-    int tokens;                 // of a workgroup: blockIdx.y says which
-    uint32_t magic;             // of the division by the vectors of a row (whole K in LDS)
-};
-
-// Groups of a batch: what a wave holds of the weights, each refilled with the
-// next batch's as soon as it has been used.
-template <int G>
-constexpr int kHeld = 512 / G;
 
 // Groups of 64 go in pairs: 128 columns are a wave's unit in any case.
 template <int G>
@@ -604,102 +589,54 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES == 16 ? 4 : 2) w4_chunk_kern
     }
 }
 
-constexpr size_t kLds = 160 * 1024;
-
 template <class Kern>
-hipError_t start(Kern kern, LdsAllowed &allowed, const W4FewArgs &a, const Plan &pl, size_t lds, int resident,
-                 int threads, hipStream_t st)
+hipError_t start(Kern kern, LdsAllowed &allowed, const W4FewArgs &a, const Plan &pl, const Form &f, size_t lds,
+                 hipStream_t st)
 {
     const hipError_t err = allow_lds_here(kern, lds, allowed);
     if (err != hipSuccess)
         return err;
-    const dim3 grid(pl.turns < resident ? pl.turns : resident, (a.T + pl.tokens - 1) / pl.tokens);
-    kern<<<grid, dim3(threads), lds, st>>>(a, pl);
+    const dim3 grid(pl.turns < f.resident ? pl.turns : f.resident, (a.T + pl.tokens - 1) / pl.tokens);
+    kern<<<grid, dim3(f.waves * 64), lds, st>>>(a, pl);
     return hipGetLastError();
 }
 
-// The plan for `waves` waves a workgroup and `resident` workgroups on the chip
-// whose split takes the least time: rounds times groups a wave.
-Plan choose(const W4FewArgs &a, int units, int waves, int cb, int resident, int max_split, int step = 1)
-{
-    constexpr int held = 4;     // units of 128 columns in a batch
-    Plan pl{};
-    long long best = LLONG_MAX;
-    for (int split = 0; split <= max_split; split += step) {
-        const int per = (waves >> split) * 16 * cb;
-        const long long turns = ((long long)a.N + per - 1) / per, rounds = (turns + resident - 1) / resident;
-        const long long each = (units + (1 << split) - 1) >> split;
-        const long long cost = rounds * (each * 4 + (split ? 6 : 2));
-        if (cost < best) {
-            best = cost;
-            pl.split = split;
-            pl.turns = (int)turns;
-            pl.batches = (int)((each + held - 1) / held);
-        }
-    }
-    return pl;
-}
-
-template <class Tx, int G, bool TL, int WAVES, int TB, int CB>
-hipError_t whole(const W4FewArgs &a, int tokens, size_t lds, hipStream_t st)
+template <class Tx, int G, bool TL, int F>
+hipError_t whole(const W4FewArgs &a, int tokens, hipStream_t st)
 {
     static LdsAllowed allowed;
-    const int resident = WAVES == 8 ? 512 : 256;
-    Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, WAVES == 8 ? 3 : 4);
-    pl.tokens = tokens;
-    pl.magic = (uint32_t)(((1ull << 32) + a.K / 8 - 1) / (a.K / 8));
-    return start(w4_whole_kernel<Tx, G, TL, WAVES, TB, CB>, allowed, a, pl, lds, resident, WAVES * 64, st);
+    constexpr Form f = kForms[F];
+    const Plan pl = plan_of(f, tokens, a.K, a.N);
+    return start(w4_whole_kernel<Tx, G, TL, f.waves, f.tb, f.cb>, allowed, a, pl, f, lds_of(f, tokens, a.K, G), st);
 }
 
-template <class Tx, int G, bool TL, int WAVES, int TB, int CB, int M>
+template <class Tx, int G, bool TL, int F>
 hipError_t chunked(const W4FewArgs &a, int tokens, hipStream_t st)
 {
-    // M = 1: one, two or four waves share a chunk; M = 4: one, four or sixteen
-    constexpr int kStep = M == 1 ? 1 : 2, resident = 256, threads = WAVES * 64;
     static LdsAllowed allowed[3];
-    const size_t need = 2 * ((size_t)tokens * (64 * M * 16 + 16) + kHeld<G> * M * TB * 64);
-    const size_t lds = need > WAVES * TB * CB * 1024 ? need : WAVES * TB * CB * 1024;
-    Plan pl = choose(a, (a.K + 127) / 128, WAVES, CB, resident, 2 * kStep, kStep);
-    pl.tokens = tokens;
-    switch (pl.split / kStep) {
-    case 0:
-        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, 0>, allowed[0], a, pl, lds, resident, threads, st);
-    case 1:
-        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, kStep>, allowed[1], a, pl, lds, resident, threads,
-                     st);
+    constexpr Form f = kForms[F];
+    static_assert(f.max_split == 2 * f.step, "one instance each");
+    const Plan pl = plan_of(f, tokens, a.K, a.N);
+    const size_t lds = lds_of(f, tokens, a.K, G);
+    switch (pl.split / f.step) {
+    case 0: return start(w4_chunk_kernel<Tx, G, TL, f.waves, f.tb, f.cb, f.m, 0>, allowed[0], a, pl, f, lds, st);
+    case 1: return start(w4_chunk_kernel<Tx, G, TL, f.waves, f.tb, f.cb, f.m, f.step>, allowed[1], a, pl, f, lds, st);
     default:
-        return start(w4_chunk_kernel<Tx, G, TL, WAVES, TB, CB, M, 2 * kStep>, allowed[2], a, pl, lds, resident,
-                     threads, st);
+        return start(w4_chunk_kernel<Tx, G, TL, f.waves, f.tb, f.cb, f.m, 2 * f.step>, allowed[2], a, pl, f, lds, st);
     }
 }
 
-// tokens: of a workgroup, at most 16.
-template <class Tx, int G, bool TL>
-hipError_t one_block(const W4FewArgs &a, int tokens, hipStream_t st)
-{
-    const size_t lds = (size_t)tokens * (a.K * 2 + 16) + (size_t)(a.K / G) * 64;
-    if (lds + 8 * 1024 <= kLds / 2)
-        return whole<Tx, G, TL, 8, 1, 1>(a, tokens, lds, st);
-    if (lds + 16 * 1024 <= kLds)
-        return whole<Tx, G, TL, 16, 1, 1>(a, tokens, lds, st);
-    return chunked<Tx, G, TL, 16, 1, 1, 4>(a, tokens, st);
-}
-
-// More than 16 tokens share each weight's unpacking in one workgroup, unless there
-// are so few channels that workgroups of 16 or of 32 tokens each (which read the
-// same weights, from the caches but for one of them) still run all at once: 64
-// tokens, K = 2816: 1024 channels 7 us in blocks of 16, 11 in 32, 18 whole; 8192
-// channels 26, 12 and 19; 16384 channels 36, 24 and 21.
 template <class Tx, int G, bool TL>
 hipError_t by_tokens(const W4FewArgs &a, hipStream_t st)
 {
-    constexpr int kChip = 256;
-    const long long by16 = (a.T + 15) / 16 * ((a.N + 15LL) / 16), by32 = (a.T + 31) / 32 * ((a.N + 63LL) / 64);
-    if (a.T <= 16 || by16 <= kChip)
-        return one_block<Tx, G, TL>(a, a.T < 16 ? a.T : 16, st);
-    if (a.T <= 32 || by32 <= kChip)
-        return chunked<Tx, G, TL, 16, 2, 1, 1>(a, a.T < 32 ? a.T : 32, st);
-    return chunked<Tx, G, TL, 8, 4, 2, 1>(a, a.T, st);
+    int tokens;
+    switch (form_of(a.T, a.K, a.N, G, tokens)) {
+    case kWhole8: return whole<Tx, G, TL, kWhole8>(a, tokens, st);
+    case kWhole16: return whole<Tx, G, TL, kWhole16>(a, tokens, st);
+    case kLongK: return chunked<Tx, G, TL, kLongK>(a, tokens, st);
+    case kBlocks2: return chunked<Tx, G, TL, kBlocks2>(a, tokens, st);
+    default: return chunked<Tx, G, TL, kBlocks4>(a, tokens, st);
+    }
 }
 
 template <class Tx>
