@@ -26,6 +26,7 @@
 // tokens: 16 -> 29 us) and in the columns with words and the registers they take
 // (256 rows of 4 sequences of 8000 tokens: 42 -> 64 us, 75 with masks).
 #include "element_types.hpp"
+#include "logit_cut.hpp"
 #include "logit_rules.hpp"
 #include "sampler_common.hpp"
 
@@ -35,18 +36,7 @@
 namespace dgw4 {
 namespace {
 
-// Threads of a workgroup. Long histories take the wider one: each workgroup reads
-// its rows' whole histories, so half as many of them read half as much (64
-// sequences of 60000 tokens: 80 -> 66 us, one of 120000: 37 -> 24). Short ones
-// take the narrower: more workgroups on a compute unit hide each other's steps (a
-// canvas of 4 sequences of 8000: 76 us against 80).
-constexpr int kNarrow = 256, kBroad = 512;
-constexpr int kLongHistory = 16384;
 constexpr int kJoin = 256;           // threads that join a row's parts
-
-// Columns of a tile: of a workgroup of `threads` that take E columns each; of a wave.
-constexpr int tile_of(int threads, int e) { return threads * e; }
-constexpr int part_of(int e) { return 64 * e; }
 
 // v of all lanes joined: the lanes of a row of 16 by DPP, then the four rows.
 template <class T, class F>
@@ -576,43 +566,13 @@ __global__ void __launch_bounds__(kJoin) join_kernel(LogitArgs a, int parts)
     }
 }
 
-// Columns a thread takes: few where that makes too few waves for the chip.
-constexpr int kFew = 8, kMany = 16;
-
-int per_thread(int R, int V)
-{
-    return (long long)R * ((V + part_of(kMany) - 1) / part_of(kMany)) >= 4096 ? kMany : kFew;
-}
-
-// Tiles of a row, and the rows that a workgroup takes in turn: where rows share
-// sequences, those of one lie next to each other, and the words are entered once
-// for them.
-struct Cut {
-    int tiles, rows;
-    uint32_t groups;
-};
-
-Cut cut(const LogitArgs &a, int tile, bool shared)
-{
-    Cut c;
-    c.tiles = (a.V + tile - 1) / tile;
-    const long long pairs = (long long)a.R * c.tiles, resident = 2048, most = 1 << 22;
-    long long rows = shared ? (pairs + resident - 1) / resident : 1;
-    rows = rows > 32 ? 32 : rows;
-    if (pairs / rows > most)                         // a launch has at most 2^32 threads
-        rows = (pairs + most - 1) / most;
-    c.rows = (int)rows;
-    c.groups = (uint32_t)((a.R + rows - 1) / rows * c.tiles);
-    return c;
-}
-
 bool has_history(const dgw4_logit_rules &u) { return u.tokens || u.n_bias > 0; }
 bool has_long_history(const dgw4_logit_rules &u) { return u.tokens && u.max_tokens >= kLongHistory; }
 
 template <class Tx, class Ty, int T, int E, bool HIST>
 hipError_t adjust(const LogitArgs &a, hipStream_t st)
 {
-    const Cut c = cut(a, tile_of(T, E), HIST && a.rules.row_seq);
+    const Cut c = cut(a.R, a.V, tile_of(T, E), HIST && a.rules.row_seq);
     if constexpr (sizeof(Tx) == sizeof(Ty)) {
         if (a.logits == a.out && !a.rules.scale) {
             adjust_kernel<Tx, Ty, T, E, HIST, true><<<dim3(c.groups), dim3(T), 0, st>>>(a, c.tiles, c.rows);
@@ -640,7 +600,7 @@ hipError_t adjust_sized(const LogitArgs &a, hipStream_t st)
 template <class Tx, int T, int E, bool HIST>
 hipError_t sample(const LogitArgs &a, hipStream_t st)
 {
-    const Cut c = cut(a, tile_of(T, E), HIST && a.rules.row_seq);
+    const Cut c = cut(a.R, a.V, tile_of(T, E), HIST && a.rules.row_seq);
     sample_adjusted_kernel<Tx, T, E, HIST><<<dim3(c.groups), dim3(T), 0, st>>>(a, c.tiles, c.rows);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
