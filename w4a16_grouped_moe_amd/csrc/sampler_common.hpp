@@ -1,5 +1,5 @@
-// What the samplers share (not part of the ABI): the noise, the order of
-// candidates and the partial of a part of a row.
+// What the samplers share (not part of the ABI): the noise and the partial of a
+// part of a row.
 #pragma once
 
 #include "dgw4_internal.hpp"
@@ -55,40 +55,6 @@ __device__ inline float gumbel(uint32_t w)
     const float u = ((float)(w >> 9) + 0.5f) * (1.0f / 8388608.0f);
     const float e = -kLn2 * __builtin_amdgcn_logf(u);
     return -kLn2 * __builtin_amdgcn_logf(e);
-}
-
-// better(a, b): larger value, or the same value at a smaller index (selects,
-// no branches)
-__device__ inline void take_best(float &v, int &i, float v2, int i2)
-{
-    const bool b = (v2 > v) | ((v2 == v) & (i2 < i));
-    v = b ? v2 : v;
-    i = b ? i2 : i;
-}
-
-// merge of two log-sum-exp partials (either may be empty: z == 0)
-__device__ inline void merge_lse(float &m, float &z, float &s, float m2, float z2, float s2)
-{
-    if (z2 == 0.0f)
-        return;
-    if (z == 0.0f) {
-        m = m2;
-        z = z2;
-        s = s2;
-        return;
-    }
-    const float mm = fmaxf(m, m2);
-    const float a = __expf(m - mm), b = __expf(m2 - mm);
-    s = a * (s + (m - mm) * z) + b * (s2 + (m2 - mm) * z2);
-    z = a * z + b * z2;
-    m = mm;
-}
-
-__device__ inline void merge_partial(Partial &p, const Partial &q)
-{
-    merge_lse(p.m, p.z, p.s, q.m, q.z, q.s);
-    take_best(p.av, p.ai, q.av, q.ai);
-    take_best(p.sv, p.si, q.sv, q.si);
 }
 
 }  // namespace
