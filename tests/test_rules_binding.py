@@ -52,3 +52,10 @@ def test_rules_of_no_sequences():
         assert dg.lib().dgw4_adjust_logits(None, 0, 0, 40, 40, rules._ref, None, 0, 40, None) == B.OK
     one = dg.LogitRules(bias_ids=_ints(1, 4), bias=torch.zeros(1, 4))
     assert (one._c.sequences, one._c.n_bias) == (1, 4)
+
+
+def test_masks_of_either_sign():
+    for dtype in (torch.int32, torch.uint32):
+        B._logits(torch.zeros(3, 40), dg.LogitRules(mask=torch.zeros((3, 2), dtype=dtype)), HOST)
+    with pytest.raises(TypeError):
+        dg.LogitRules(mask=torch.zeros((3, 2), dtype=torch.int64))
