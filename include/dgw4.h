@@ -554,6 +554,16 @@ DGW4_API int dgw4_w8a8_linear_tokens(const void *x, int x_type, int T, int K, lo
  * DGW4_ERR_UNSUPPORTED for T > 64, other group sizes, x_type DGW4_F32,
  * K > 2^24 or N > 2^31 - 257; DGW4_ERR_INVALID_ARG for the rest. Enqueued on
  * `stream`, no host sync.
+ * Of the calls that dgw4_w4a16_linear takes too (fp16 x and y, rows without
+ * gaps, N % 16 == 0, at most 64 groups) this one is the faster, by up to 3
+ * times, except at K = 2816, the width that the other's kernel is laid out for.
+ * There the other is the faster for 17 to 64 tokens of up to 16384 channels and
+ * for up to 32 tokens of 16384 to 32768 channels (not for one of 16384); with
+ * row-major weights in groups of 128 also for up to 32 tokens of 65536 and up to
+ * 8 of 262144. In us, this one / the other, tiled, g 128: 4096 channels with 16,
+ * 17 and 64 tokens 7.5 / 8.2, 10.7 / 10.1 and 11.7 / 10.4; 16384 with 8 and 64
+ * 10.6 / 9.5 and 21 / 16.7; 32768 with 32 and 33 19.4 / 18.9 and 24.8 / 26.4;
+ * 262144 with 1, 16 and 64 68 / 71, 86 / 90 and 159 / 200.
  */
 DGW4_API int dgw4_w4a16_linear_few(const void *x, int x_type, int T, int K, long long ldx,
                                    const uint8_t *q, const uint16_t *s, const uint16_t *z, int N,
@@ -580,7 +590,10 @@ DGW4_API int dgw4_w4a16_linear_few(const void *x, int x_type, int T, int K, long
  *   row_seq     int32 [R]; outside [0, sequences): the row has no rules but
  *               its mask. NULL: row r is sequence r (sequences >= R, or 0)
  *   tokens      int32 [sequences, max_tokens], rows ld_tokens apart; NULL:
- *               none, and no penalties then. 1 <= max_tokens < 2^21
+ *               none, and no penalties then. 1 <= max_tokens < 2^21, which
+ *               from 16384 on has the kernels laid out for long histories (a
+ *               tenth slower for short ones in a large buffer; the results
+ *               are the same)
  *   lengths     int32 [sequences]; prompt_lengths int32 [sequences] or NULL
  *               (0: all tokens count as generated)
  *   repetition, frequency, presence, scale   fp32 [sequences] or NULL

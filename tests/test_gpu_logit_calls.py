@@ -61,3 +61,21 @@ def test_two_host_threads_call_by_call():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("R,V,S", [(3, 5000, 3), (40, 70000, 40), (1500, 9000, 7)])
+def test_a_larger_buffer_changes_nothing(R, V, S):
+    # the same tokens in a buffer of long contexts, and in a view of its columns in use
+    rng = np.random.default_rng(V)
+    u = {k: v.cuda() for k, v in rules_ref.random_rules(rng, R, V, S=S, L=300, bias=4).items()}
+    u["lengths"].clamp_(max=300)
+    x = torch.from_numpy((rng.standard_normal((R, V)) * 3).astype(np.float32)).cuda()
+    wide = torch.full((S, 40000), 7, dtype=torch.int32, device="cuda")
+    wide[:, :300] = u["tokens"]
+    want = None
+    for tokens in (u["tokens"], wide[:, :300], wide):
+        rules = dg.LogitRules(**{**u, "tokens": tokens})
+        got = (*dg.sample_adjusted(x, rules, 8), dg.adjust_logits(x, rules))
+        want = want or got
+        assert same_bits(got[0], want[0]) and same_bits(got[3], want[3])
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])

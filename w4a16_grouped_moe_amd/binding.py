@@ -781,7 +781,8 @@ def w4a16_linear_few(x: torch.Tensor, w: tuple, out: torch.Tensor | None = None,
     [N, K/g], z fp16 [N, K/g], g) as for w4a16_linear, any N, or its pack_tiled
     form. Returns y [T, N] of ``dtype`` (fp16, bf16 or fp32; x's type when not
     given), or written into ``out``, whose type counts then. See
-    dgw4_w4a16_linear_few in include/dgw4.h."""
+    dgw4_w4a16_linear_few in include/dgw4.h, also for the calls that
+    w4a16_linear is the faster for (K = 2816, 17 to 64 tokens, few channels)."""
     q, s, z, g = w
     d = _gpu(x, "x")
     px, T, K, ldx = _rows(x, "x", _HALVES, d)

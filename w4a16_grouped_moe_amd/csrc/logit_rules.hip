@@ -12,19 +12,26 @@
 // have a word: the wave's lanes take those columns in turns of 64, whoever holds
 // them, and the logits go through LDS there and back. (Each lane with its own
 // columns, one at a time, waits for the lane that has most: a canvas of 256 rows
-// and 4 sequences 84 us against 75, 64 histories of 60000 tokens 70 against 65; in
-// place with nothing else changed it was the better by 20 us to 21.)
+// and 4 sequences 84 us against 76, 64 histories of 60000 tokens 70 against 65; in
+// place with nothing else changed it was the better by 20 us to 21, with 1000
+// tokens a row by 28.6 to 29.4.)
 //
 // A wave's part of a row (the maximum, its first place, sums of exp relative to
 // it, the best score) goes to the workspace; a second kernel joins a row's parts.
 // Every order is fixed, so results are bitwise reproducible.
 //
-// Bounds: adjusting is a copy, 256 x 262144 fp32 101 us (5.3 TB/s; in place, with
-// nothing changed but a few columns, 64 x 262144 21 us). The sampler without rules
-// reads 6.4 TB/s (256 x 262144, entropy and argmax 42 us); history costs half or more
-// on top, in the steps that make the words (64 rows of own sequences of 1000
-// tokens: 16 -> 29 us) and in the columns with words and the registers they take
-// (256 rows of 4 sequences of 8000 tokens: 42 -> 64 us, 75 with masks).
+// Bounds (all figures of this file: replays of a graph over logits that change from
+// call to call, medians, V = 262144, fp32 where nothing else is said): adjusting is
+// a copy, 256 rows 101 us (5.3 TB/s; fp16 to itself 57, 4.7 TB/s). In place with
+// nothing changed but a few columns it is not: 64 rows of 1000 tokens 21 us, of
+// which a few columns' lines would be one; each of 4096 workgroups clears its words
+// and reads the row's tokens. The sampler without rules reads 256 rows in 48 us (44
+// at best, 6.1 TB/s); history costs half or more on top, in the steps that make the
+// words (64 rows of own sequences of 1000 tokens, greedy: 16 -> 29 us) and in the
+// columns with words and the registers they take (256 rows of 4 sequences of 8000
+// tokens: 48 -> 65 us, 76 with masks): with history and 16 columns a thread the
+// sampler keeps 62 of its scalars, the rules' pointers among them, in lanes of
+// vector registers, adjusting 30 to 34.
 #include "element_types.hpp"
 #include "logit_cut.hpp"
 #include "logit_rules.hpp"
@@ -225,8 +232,8 @@ __device__ inline uint32_t with_words(const uint32_t *words, int step)
 
 // A wave's columns with words, dealt out over its lanes: lane i has the i-th of each
 // 64, its place in the tile's words and its word. Two turns: one sends the waves of
-// long histories the other way (64 of 60000 tokens: 72 us against 65), three or four
-// take registers from all (canvas of 256 rows in fp16: 100 and 103 us against 96).
+// long histories the other way (64 of 60000 tokens: 72 us against 66), three or four
+// take registers from all (canvas of 256 rows in fp16: 103 and 107 us against 97).
 constexpr int kDealt = 2;
 
 struct Dealt {
@@ -317,7 +324,10 @@ __device__ inline void follow_rules(float (&l)[N * W], const Dealt &d, uint32_t 
         l[e] = rounded_product(l[e], q.scale);
 }
 
-// E columns a thread; SPARSE: in place and no scale, so only what changes is read and written.
+// E columns a thread; SPARSE: in place and no scale, so only what changes is read and
+// written. Five waves a SIMD for 16-bit logits (a batch of 48 rows 12.5 -> 10.6 us);
+// out of place with history and 16 columns, fp16 then spills two vector registers,
+// 12 bytes of scratch a lane.
 template <class Tx, class Ty, int kThreads, int E, bool HIST, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kernel(LogitArgs a, int tiles, int rows)
 {

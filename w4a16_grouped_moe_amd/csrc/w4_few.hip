@@ -26,13 +26,15 @@
 // at small sizes and level at the LM head.
 //
 // Up to 16 tokens whose x fits LDS whole (w4_whole_kernel): tiled weights, g 128,
-// in a graph: 1 token x 4096 channels x 2816 5.0 us, 16 x 11264 x 4096 11.8 (the
-// activations' way into every workgroup's LDS, 131 KB, is part of it), LM head 1 /
-// 5 / 16 tokens 68 / 72 / 79 us (5.8 / 5.4 / 5.0 TB/s). Else x goes through LDS in
-// chunks (w4_chunk_kernel): 2 x 4096 x 65536 33 us, LM head 32 / 64 tokens 103 /
-// 151 us, where unpacking, the scales' fma and the MFMA share the time (a chunk of
-// 512 columns of 64 tokens takes a workgroup 2.2 us, 0.8 for each group's products
-// of a wave, the rest the staging of x).
+// fp16, in a graph over rotated matrices (medians): 1 token x 4096 channels x 2816
+// 5.0 us, 16 x 11264 x 4096 11.6 (the activations' way into every workgroup's LDS,
+// 131 KB, is part of it; 176 workgroups of 64 channels, so 80 of the chip's 256
+// compute units have none), LM head 1 / 5 / 16 tokens 64 / 68 / 82 us (6.1 / 5.8 /
+// 4.8 TB/s). Else x goes through LDS in chunks (w4_chunk_kernel): 2 x 4096 x 65536
+// 32 us, LM head 32 / 64 tokens 106 / 155 us, where unpacking, the scales' fma and
+// the MFMA share the time (a chunk of 512 columns of 64 tokens takes a workgroup
+// 2.2 us, 0.8 for each group's products of a wave, the rest the staging of x, again
+// for each turn of channels).
 #include "gemm_common.hpp"
 #include "step_end.hpp"
 #include "w4_few_plan.hpp"

@@ -54,9 +54,15 @@ inline size_t lds_of(const Form &f, int tokens, int K, int g)
 //
 // More than 16 tokens share each weight's unpacking in one workgroup, unless there
 // are so few channels that workgroups of 16 or of 32 tokens each (which read the
-// same weights, from the caches but for one of them) still run all at once: 64
-// tokens, K = 2816: 1024 channels 7 us in blocks of 16, 11 in 32, 18 whole; 8192
-// channels 26, 12 and 19; 16384 channels 36, 24 and 21.
+// same weights, from the caches but for one of them) still run all at once. In a
+// graph, us in blocks of 16 / of 32 / whole:
+//   64 tokens, K 2816: 1024 channels 7.0 / 11.3 / 17.8, 8192 26 / 12.4 / 18.5,
+//     16384 35 / 25 / 20
+//   64 tokens, K 8192: 1024 channels 11 / 23 / 38, 8192 69 / 26 / 39, 16384 80 / 55 / 43
+//   32 tokens, K 1408: 2048 channels 5.2 / 8.2 / 10, 8192 12 / 8.5 / 10
+// Just past a border the form before it would still be the faster for some: 32
+// tokens, K 1408, 2064 channels 6.6 / 8.2, 20 tokens, K 8192, 2064 channels 15 / 21
+// (of 132 sizes the worst; nine lose more than 15%, all within twice a border).
 inline int form_of(int T, int K, int N, int g, int &tokens)
 {
     constexpr int kChip = 256;
@@ -75,7 +81,12 @@ inline int form_of(int T, int K, int N, int g, int &tokens)
     return kBlocks4;
 }
 
-// The plan whose split takes the least time: rounds times groups a wave.
+// The plan whose split takes the least time by an estimate: rounds of the chip times
+// what a wave does in one, in quarters of a unit of 128 columns: four a unit, and
+// for the turn's beginning and end half a unit, or one and a half where waves join
+// in LDS (both set by hand). Against each split by itself, 23 sizes of 1 to 64
+// tokens: 5% slower than the best on average, 16% at worst (16 x 8192 x 8192 21 us
+// against 18; two timings of one split are up to 10% apart).
 inline Plan plan_of(const Form &f, int tokens, int K, int N)
 {
     constexpr int held = 4;     // units of 128 columns in a batch
