@@ -21,7 +21,7 @@
 // Every order is fixed, so results are bitwise reproducible.
 //
 // Bounds (all figures of this file: replays of a graph over logits that change from
-// call to call, medians, V = 262144, fp32 where nothing else is said): adjusting is
+// call to call, medians, 262144 columns of fp32 where nothing else is said): adjusting is
 // a copy, 256 rows 101 us (5.3 TB/s; fp16 to itself 57, 4.7 TB/s). In place with
 // nothing changed but a few columns it is not: 64 rows of 1000 tokens 21 us, of
 // which a few columns' lines would be one; each of 4096 workgroups clears its words
@@ -325,9 +325,11 @@ __device__ inline void follow_rules(float (&l)[N * W], const Dealt &d, uint32_t 
 }
 
 // E columns a thread; SPARSE: in place and no scale, so only what changes is read and
-// written. Five waves a SIMD for 16-bit logits (a batch of 48 rows 12.5 -> 10.6 us);
-// out of place with history and 16 columns, fp16 then spills two vector registers,
-// 12 bytes of scratch a lane.
+// written. Five waves a SIMD for 16-bit logits hide the words' making (48 rows of
+// 100003 bf16 with every rule 15.3 -> 12.0 us), though a canvas of shared words goes
+// better with four (256 rows of fp16 to fp32 90 us against 96, to fp16 56 against
+// 58): out of place with history and 16 columns, fp16 spills two vector registers
+// under five, 12 bytes of scratch a lane.
 template <class Tx, class Ty, int kThreads, int E, bool HIST, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, sizeof(Tx) == 2 ? 5 : 4) adjust_kernel(LogitArgs a, int tiles, int rows)
 {
